@@ -520,6 +520,120 @@ int tpc_group_backward(const tpc_plan* plan, const tpc_group_shape* shape, const
 /* Synchronises `stream`, returns and clears the first device-side error of the group's kernels. */
 int tpc_group_status(const tpc_plan* plan, const tpc_group_shape* shape, void* ws, tpc_stream_t stream);
 
+/* ------------------------------------------------------------------ token-by-token generation */
+/*
+ * The group's layers one token at a time, for sampling the rollouts that the tree calls train on
+ * (HARTS Figure 1: trajectories branch from shared prefixes): a recurrent KDA step on a cache of
+ * states, and latent attention in its absorbed form over a paged cache of latents.
+ *
+ * A batch holds n_seqs sequences and n_rows new token rows, ordered by sequence: sequence b owns
+ * rows row_start[b] .. row_start[b + 1] - 1 (none, one or many; row_start non-decreasing, within
+ * 0 .. n_rows).  row_start NULL: one row each, n_rows == n_seqs.  Rows outside every sequence are
+ * neither read nor written.  kv_len[b] counts the cached tokens of sequence b, its new rows
+ * included, so new row i of m is at position kv_len[b] - m + i; a row at a negative position
+ * (kv_len 0: a padding entry of the batch) has no token.  row_start, kv_len and the block table are
+ * device memory, read when the kernels run, so that a captured graph can be replayed with new values.
+ *
+ * status (optional device int) receives TPC_ERR_DEVICE_CHECK if an index is outside its range (the
+ * entry is then skipped or bounded, never followed) and TPC_ERR_TIMEOUT if a bounded wait ran out.
+ */
+typedef struct tpc_rows {
+  int32_t n_rows, n_seqs;
+  const int32_t* row_start; /* [n_seqs + 1] or NULL */
+  const int32_t* kv_len;    /* [n_seqs]; not read by tpc_kda_step */
+} tpc_rows;
+
+/*
+ * Recurrent KDA: for every sequence b and head, S = state[src[b]]; each new row in order:
+ *   S <- (I - beta k k^T) Diag(exp(g)) S + beta k v^T,  o = S^T q;
+ * then state[dst[b]] = S (also when the sequence has no new row).  The states are fp32 [n_slots, H,
+ * d, d], the layout of tpc_kda_forward's final_state, which therefore serves as the cache.  fp32
+ * arithmetic throughout; o is rounded once to out_dtype.
+ *   src, dst: device int32 [n_seqs].  Several sequences may read one slot (branches of a rollout);
+ *   dst NULL updates src in place.  A sequence whose src is negative is a padding entry: nothing of
+ *   it is read or written.  A dst that occurs twice, or that another sequence reads, is a race
+ *   between sequences: with a status word it records TPC_ERR_DEVICE_CHECK, and those slots and
+ *   rows hold unspecified values.
+ *   shape: dk == dv in {32, 64, 128}, H >= 1, in_dtype TPC_F32 or TPC_BF16 (q, k, v, g, beta).
+ *   q, k, v, g: [n_rows, H, d], beta [n_rows, H], 16-byte aligned.  g may be any value <= 0,
+ *   -infinity included (the channel's state is dropped).
+ * Errors: TPC_ERR_NULL, TPC_ERR_BAD_SHAPE, TPC_ERR_UNSUPPORTED, TPC_ERR_CUDA.
+ */
+typedef struct tpc_kda_step_io {
+  const void* q; const void* k; const void* v; const void* g; const void* beta;
+  float* state;
+  int32_t n_slots;
+  const int32_t* src;
+  const int32_t* dst;
+  void* o; /* [n_rows, H, dv] out_dtype */
+} tpc_kda_step_io;
+int tpc_kda_step(const tpc_kda_shape* shape, const tpc_rows* rows, const tpc_kda_step_io* io, int32_t* status,
+                 tpc_stream_t stream);
+
+/*
+ * Paged cache of latents: page p holds page_size tokens of TPC_LATENT_WIDTH bf16 each, the latent c
+ * (512) then the rotated rotary key (64).  Token j of sequence b is token j mod page_size of page
+ * block_table[b * max_pages + j / page_size]; sequences may share pages (common prefixes).
+ * page_size: 16, 32 or a multiple of 64.  data 16-byte aligned.
+ */
+#define TPC_LATENT_DIM 512
+#define TPC_LATENT_ROPE 64
+#define TPC_LATENT_HEAD 128
+#define TPC_LATENT_WIDTH 576
+typedef struct tpc_latent_cache {
+  void* data; /* [n_pages][page_size][576] bf16 */
+  int32_t n_pages, page_size;
+  const int32_t* block_table; /* device [n_seqs][max_pages] */
+  int32_t max_pages;
+} tpc_latent_cache;
+
+/*
+ * Writes the new rows into the cache: the latent c, and the shared rotary key rotated at the row's
+ * position (half-split, base 10000, angles in double precision), each rounded once to bf16.
+ *   c: row t at c + t * ld_c, 512 elements; kr: row t at kr + t * ld_kr, 64 elements, of in_dtype
+ *   (TPC_F32 or TPC_BF16); 16-byte aligned, leading dimensions multiples of 16 bytes, so that both
+ *   may be slices of a projection.
+ * Rows without a token are skipped.  Two rows that write one cached token (a page of two
+ * sequences that both write it) race: with a status word that records TPC_ERR_DEVICE_CHECK.
+ */
+int tpc_latent_append(const tpc_latent_cache* cache, const tpc_rows* rows, const void* c, int64_t ld_c,
+                      const void* kr, int64_t ld_kr, int32_t in_dtype, int32_t* status, tpc_stream_t stream);
+
+/*
+ * Queries of the absorbed form: qa[t][h] = [ q_nope W_k[h] (512) | rotated q_rope (64) ], bf16, from
+ * q row t, head h at q + t * ld_q + 192 h (128 no-position then 64 rotary dimensions, bf16) and the
+ * group's W_b [2 * 128 * H][512] (rows 128 h .. 128 h + 127 are head h's W_k).  Products in fp32,
+ * rounded once.  The rotation takes the row's position as it is, negative ones included.  q and
+ * W_b 16-byte aligned, ld_q a multiple of 8.  The scores qa . [c | kr] are those of the expanded
+ * form q . [k_nope | kr].
+ */
+int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld_q, const void* w_b, void* qa,
+                      int32_t* status, tpc_stream_t stream);
+
+/*
+ * Absorbed latent attention of the new rows over the cache (which holds them: tpc_latent_append
+ * first): row at position p reads cached tokens 0 .. p of its sequence,
+ *   o[t][h] = sum_j softmax_j(scale qa[t][h] . cache_j) c_j   (bf16 [n_rows][H][512]),
+ *   lse[t][h] = log sum_j exp(scale qa[t][h] . cache_j)        (fp32 [n_rows][H], natural log).
+ * A row without a token gets o = 0 and lse = -infinity.  Tokens past kv_len are never used,
+ * whatever the page holds there.  Scores, softmax statistics and sums in fp32; the weights enter
+ * their product as bf16.  qa: [n_rows][H][576] bf16, 16-byte aligned, 1 <= H <= 128.
+ *   scratch: tpc_latent_attn_scratch_bytes(H) bytes, 256-byte aligned, used by one call at a time.
+ * Deterministic: the same call gives the same bits.  A block table entry outside 0 .. n_pages - 1
+ * or a kv_len beyond max_pages * page_size records TPC_ERR_DEVICE_CHECK (the sequence's rows are
+ * then unspecified).
+ */
+size_t tpc_latent_attn_scratch_bytes(int32_t H);
+int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t H, float scale, const void* qa,
+                    void* o, float* lse, void* scratch, size_t scratch_bytes, int32_t* status, tpc_stream_t stream);
+
+/*
+ * Head outputs of the absorbed form: out[t][h] = W_v[h] o[t][h] (bf16 [n_rows][H][128]) from o
+ * [n_rows][H][512] bf16 and W_b as above (rows 128 H + 128 h .. are head h's W_v).  fp32 sums.
+ */
+int tpc_latent_expand(int32_t n_rows, int32_t H, const void* o, const void* w_b, void* out, int32_t* status,
+                      tpc_stream_t stream);
+
 /* ------------------------------------------------------------------ allocation-free forward */
 /* Bytes of device scratch built into the library for tpc_kda_forward_static (64 MiB). */
 #define TPC_STATIC_SCRATCH_BYTES (64u << 20)

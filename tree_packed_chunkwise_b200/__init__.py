@@ -84,6 +84,22 @@ class AttnLo(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("d_o", ctypes.c_void_p)]
 
 
+class Rows(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("row_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p)]
+
+
+class KdaStepIO(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("g", ctypes.c_void_p),
+                ("beta", ctypes.c_void_p), ("state", ctypes.c_void_p), ("n_slots", ctypes.c_int32),
+                ("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("o", ctypes.c_void_p)]
+
+
+class LatentCache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("max_pages", ctypes.c_int32)]
+
+
 class GroupShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("D", "H", "d_head", "d_rope", "d_latent", "n_kda", "reuse_forward")]
 
@@ -148,6 +164,14 @@ SIGNATURES = {
     "tpc_group_backward": (ctypes.c_int, [_V, _P(GroupShape), _P(GroupWeights), _V, _V, _V, _V, _P(GroupGrads), _V,
                                           ctypes.c_size_t, _V]),
     "tpc_group_status": (ctypes.c_int, [_V, _P(GroupShape), _V, _V]),
+    "tpc_kda_step": (ctypes.c_int, [_P(KdaShape), _P(Rows), _P(KdaStepIO), _V, _V]),
+    "tpc_latent_append": (ctypes.c_int, [_P(LatentCache), _P(Rows), _V, ctypes.c_int64, _V, ctypes.c_int64,
+                                         ctypes.c_int32, _V, _V]),
+    "tpc_latent_absorb": (ctypes.c_int, [_P(Rows), ctypes.c_int32, _V, ctypes.c_int64, _V, _V, _V, _V]),
+    "tpc_latent_attn_scratch_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+    "tpc_latent_attn": (ctypes.c_int, [_P(LatentCache), _P(Rows), ctypes.c_int32, ctypes.c_float, _V, _V, _V, _V,
+                                       ctypes.c_size_t, _V, _V]),
+    "tpc_latent_expand": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _V, _V, _V, _V, _V]),
     "tpc_profile_enable": (None, [ctypes.c_int]),
     "tpc_profile_read": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_size_t]),
     "tpc_launch_count": (ctypes.c_longlong, []),
@@ -790,3 +814,200 @@ def tpc_group_backward(plan: Plan, weights, x, h, dy, ws, dx=None, grads=None, s
 def tpc_group_status(plan: Plan, ws, n_kda: int = 3, stream=None) -> int:
     sh = group_shape(n_kda)
     return int(lib().tpc_group_status(plan.handle, ctypes.byref(sh), _ptr(ws), _stream_ptr(stream)))
+
+
+# ------------------------------------------------------------------------------------ token-by-token generation
+LATENT_DIM, LATENT_ROPE, LATENT_HEAD, LATENT_WIDTH = 512, 64, 128, 576
+
+
+def _want(name, t, shape, dtypes, dev, contiguous=True):
+    """Raises TpcError (TPC_ERR_BAD_SHAPE) unless t has the shape, one of the dtypes and lives on dev."""
+    if tuple(t.shape) != shape:
+        raise TpcError(2, f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype not in dtypes:
+        raise TpcError(2, f"{name} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.device != dev:
+        raise TpcError(2, f"{name} is on {t.device}, not on {dev}")
+    if contiguous and not t.is_contiguous():
+        raise TpcError(2, f"{name} is not contiguous")
+
+
+def _decode_device(t):
+    """t's device, which must be the current CUDA device."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise TpcError(2, f"tensors are on {t.device}, not on the current CUDA device")
+    return t.device
+
+
+def _decode_rows(n_rows, row_start, kv_len, n_seqs, dev, status):
+    import torch
+    i32 = (torch.int32,)
+    if row_start is None and n_rows != n_seqs:
+        raise TpcError(2, f"{n_rows} rows for {n_seqs} sequences need row_start")
+    if row_start is not None:
+        _want("row_start", row_start, (n_seqs + 1,), i32, dev)
+    if kv_len is not None:
+        _want("kv_len", kv_len, (n_seqs,), i32, dev)
+    if status is not None:
+        _want("status", status, tuple(status.shape), i32, dev)
+        if status.numel() < 1:
+            raise TpcError(2, "status needs one element")
+    return Rows(n_rows, n_seqs, None if row_start is None else row_start.data_ptr(),
+                None if kv_len is None else kv_len.data_ptr())
+
+
+def _latent_cache(cache, block_table, n_seqs, dev):
+    import torch
+    if cache.dim() != 3:
+        raise TpcError(2, f"cache must be [n_pages, page_size, {LATENT_WIDTH}], got {tuple(cache.shape)}")
+    _want("cache", cache, (cache.shape[0], cache.shape[1], LATENT_WIDTH), (torch.bfloat16,), dev)
+    if block_table.dim() != 2:
+        raise TpcError(2, f"block_table must be [n_seqs, max_pages], got {tuple(block_table.shape)}")
+    _want("block_table", block_table, (n_seqs, block_table.shape[1]), (torch.int32,), dev)
+    return LatentCache(cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(), block_table.shape[1])
+
+
+def _new(stream, *shape, dtype, dev):
+    """An uninitialised tensor of the call's stream: its memory is reused in that stream's order."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def tpc_kda_step(state, src, q, k, v, g, beta, dst=None, row_start=None, out_dtype=None, o=None, status=None,
+                 stream=None):
+    """Advances cached KDA states by the batch's new rows (include/tpc.h); returns o [n_rows, H, d].
+    state: fp32 [n_slots, H, d, d], updated; src: int32 [n_seqs] slot read by each sequence; dst: slot written
+    (default: in place); row_start: int32 [n_seqs + 1] rows of each sequence (default: one each)."""
+    import torch
+    dev = _decode_device(state)
+    if q.dim() != 3 or state.dim() != 4:
+        raise TpcError(2, f"q must be [n_rows, H, d] and state [n_slots, H, d, d], got {tuple(q.shape)} and {tuple(state.shape)}")
+    n, H, d = q.shape
+    out_dtype = out_dtype or (o.dtype if o is not None else q.dtype)
+    both, one = (torch.bfloat16, torch.float32), (q.dtype,)
+    _want("q", q, (n, H, d), both, dev)
+    for name, t in (("k", k), ("v", v), ("g", g)):
+        _want(name, t, (n, H, d), one, dev)
+    _want("beta", beta, (n, H), one, dev)
+    _want("state", state, (state.shape[0], H, d, d), (torch.float32,), dev)
+    n_seqs = src.shape[0] if src.dim() == 1 else -1
+    _want("src", src, (n_seqs,), (torch.int32,), dev)
+    if dst is not None:
+        _want("dst", dst, (n_seqs,), (torch.int32,), dev)
+    rows = _decode_rows(n, row_start, None, n_seqs, dev, status)
+    if o is None:
+        o = _new(stream, n, H, d, dtype=out_dtype, dev=dev)
+    else:
+        _want("o", o, (n, H, d), (out_dtype,), dev)
+    if out_dtype not in both:
+        raise TpcError(2, f"out_dtype {out_dtype} is neither bf16 nor fp32")
+    shape = kda_shape(H, d, _dtype_code(q), TPC_BF16 if out_dtype == torch.bfloat16 else TPC_F32)
+    io = KdaStepIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(),
+                   state.shape[0], src.data_ptr(), None if dst is None else dst.data_ptr(), o.data_ptr())
+    _check(lib().tpc_kda_step(ctypes.byref(shape), ctypes.byref(rows), ctypes.byref(io), _ptr(status),
+                              _stream_ptr(stream)))
+    return o
+
+
+def tpc_latent_append(cache, block_table, kv_len, c, kr, row_start=None, status=None, stream=None):
+    """Writes the new rows' latents and rotated keys into the paged cache (include/tpc.h).  cache: bf16 [n_pages,
+    page_size, 576]; block_table: int32 [n_seqs, max_pages]; kv_len: int32 [n_seqs], new rows included; c [n_rows,
+    512] and kr [n_rows, 64]: bf16 or fp32, rows may be slices of a wider tensor."""
+    import torch
+    dev = _decode_device(cache)
+    if kv_len.dim() != 1 or c.dim() != 2:
+        raise TpcError(2, f"kv_len must be [n_seqs] and c [n_rows, {LATENT_DIM}]")
+    n = c.shape[0]
+    lc = _latent_cache(cache, block_table, kv_len.shape[0], dev)
+    _want("c", c, (n, LATENT_DIM), (torch.bfloat16, torch.float32), dev, contiguous=False)
+    _want("kr", kr, (n, LATENT_ROPE), (c.dtype,), dev, contiguous=False)
+    if n and (c.stride(1) != 1 or kr.stride(1) != 1):
+        raise TpcError(2, "the rows of c and kr must be contiguous")
+    rows = _decode_rows(n, row_start, kv_len, kv_len.shape[0], dev, status)
+    ld = lambda t, w: t.stride(0) if n > 1 else w  # the stride of a single row says nothing
+    _check(lib().tpc_latent_append(ctypes.byref(lc), ctypes.byref(rows), _ptr(c), ld(c, LATENT_DIM), _ptr(kr),
+                                   ld(kr, LATENT_ROPE), _dtype_code(c), _ptr(status), _stream_ptr(stream)))
+
+
+def tpc_latent_absorb(q, w_b, kv_len, row_start=None, qa=None, status=None, stream=None):
+    """Absorbed queries qa [n_rows, H, 576] (bf16) of q [n_rows, H, 192] (bf16; the rows may be slices of a wider
+    tensor) and the group's w_b [2 * 128 * H, 512], the rotary part turned at the rows' positions (include/tpc.h)."""
+    import torch
+    dev = _decode_device(q)
+    bf = (torch.bfloat16,)
+    if q.dim() != 3 or kv_len.dim() != 1:
+        raise TpcError(2, f"q must be [n_rows, H, {LATENT_HEAD + LATENT_ROPE}] and kv_len [n_seqs]")
+    n, H, _ = q.shape
+    qk = LATENT_HEAD + LATENT_ROPE
+    _want("q", q, (n, H, qk), bf, dev, contiguous=False)
+    if n and (q.stride(2) != 1 or (H > 1 and q.stride(1) != qk)):
+        raise TpcError(2, "the rows of q must be contiguous")
+    _want("w_b", w_b, (2 * LATENT_HEAD * H, LATENT_DIM), bf, dev)
+    rows = _decode_rows(n, row_start, kv_len, kv_len.shape[0], dev, status)
+    if qa is None:
+        qa = _new(stream, n, H, LATENT_WIDTH, dtype=torch.bfloat16, dev=dev)
+    else:
+        _want("qa", qa, (n, H, LATENT_WIDTH), bf, dev)
+    _check(lib().tpc_latent_absorb(ctypes.byref(rows), H, _ptr(q), q.stride(0) if n > 1 else H * qk, _ptr(w_b),
+                                   _ptr(qa), _ptr(status), _stream_ptr(stream)))
+    return qa
+
+
+def latent_attn_scratch(H, device="cuda"):
+    """Scratch of tpc_latent_attn for H heads (used by one call at a time)."""
+    import torch
+    return torch.empty(int(lib().tpc_latent_attn_scratch_bytes(H)), dtype=torch.uint8, device=device)
+
+
+def tpc_latent_attn(qa, cache, block_table, kv_len, scale, row_start=None, o=None, lse=None, scratch=None,
+                    status=None, stream=None):
+    """Absorbed latent attention of the new rows over the paged cache (include/tpc.h); returns (o [n_rows, H, 512]
+    bf16, lse [n_rows, H] fp32).  qa: bf16 [n_rows, H, 576] of tpc_latent_absorb."""
+    import torch
+    dev = _decode_device(qa)
+    bf = (torch.bfloat16,)
+    if qa.dim() != 3 or kv_len.dim() != 1:
+        raise TpcError(2, f"qa must be [n_rows, H, {LATENT_WIDTH}] and kv_len [n_seqs]")
+    n, H, _ = qa.shape
+    _want("qa", qa, (n, H, LATENT_WIDTH), bf, dev)
+    lc = _latent_cache(cache, block_table, kv_len.shape[0], dev)
+    rows = _decode_rows(n, row_start, kv_len, kv_len.shape[0], dev, status)
+    if o is None:
+        o = _new(stream, n, H, LATENT_DIM, dtype=torch.bfloat16, dev=dev)
+    else:
+        _want("o", o, (n, H, LATENT_DIM), bf, dev)
+    if lse is None:
+        lse = _new(stream, n, H, dtype=torch.float32, dev=dev)
+    else:
+        _want("lse", lse, (n, H), (torch.float32,), dev)
+    if scratch is None:
+        scratch = _new(stream, int(lib().tpc_latent_attn_scratch_bytes(H)), dtype=torch.uint8, dev=dev)
+    else:
+        _want("scratch", scratch, tuple(scratch.shape), (torch.uint8,), dev)
+    _check(lib().tpc_latent_attn(ctypes.byref(lc), ctypes.byref(rows), H, float(scale), _ptr(qa), _ptr(o), _ptr(lse),
+                                 _ptr(scratch), scratch.numel(), _ptr(status), _stream_ptr(stream)))
+    return o, lse
+
+
+def tpc_latent_expand(o, w_b, out=None, status=None, stream=None):
+    """Head outputs [n_rows, H, 128] (bf16) of the attention's o [n_rows, H, 512] through w_b's value rows."""
+    import torch
+    dev = _decode_device(o)
+    bf = (torch.bfloat16,)
+    if o.dim() != 3:
+        raise TpcError(2, f"o must be [n_rows, H, {LATENT_DIM}]")
+    n, H, _ = o.shape
+    _want("o", o, (n, H, LATENT_DIM), bf, dev)
+    _want("w_b", w_b, (2 * LATENT_HEAD * H, LATENT_DIM), bf, dev)
+    if status is not None:
+        _want("status", status, tuple(status.shape), (torch.int32,), dev)
+    if out is None:
+        out = _new(stream, n, H, LATENT_HEAD, dtype=torch.bfloat16, dev=dev)
+    else:
+        _want("out", out, (n, H, LATENT_HEAD), bf, dev)
+    _check(lib().tpc_latent_expand(n, H, _ptr(o), _ptr(w_b), _ptr(out), _ptr(status), _stream_ptr(stream)))
+    return out

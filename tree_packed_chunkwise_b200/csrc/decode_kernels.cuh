@@ -1,0 +1,387 @@
+// Kernels of token-by-token generation: the recurrent KDA step on a cache of states, the append to
+// the paged cache of latents, and the simple forms of latent attention and its per-head products.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace tpc {
+
+constexpr int kLatDim = 512, kLatRope = 64, kLatHead = 128, kLatWidth = kLatDim + kLatRope, kLatQK = kLatHead + kLatRope;
+
+// device view of tpc_rows
+struct DecodeRows {
+  int n_rows, n_seqs;
+  const int32_t* row_start;  // NULL: row b is sequence b's
+  const int32_t* kv_len;
+};
+
+// device view of tpc_latent_cache
+struct LatentCache {
+  __nv_bfloat16* data;
+  int n_pages, page_size;
+  const int32_t* table;
+  int max_pages;
+};
+
+// Sequence that owns row t, by the whole warp: the number of sequences whose rows end at or before t,
+// found by 33-way search (one probe per lane and level, so three dependent loads reach 32,768
+// sequences).  In [0, n_seqs] whatever row_start holds, and the range shrinks on every level.
+__device__ __forceinline__ int seq_of_row(const int32_t* row_start, int n_seqs, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n_seqs;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32, j = lo + (lane + 1) * step - 1;
+    const bool ended = j < hi && row_start[j + 1] <= t;
+    lo += __popc(__ballot_sync(0xffffffffu, ended)) * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
+struct RowAt {
+  int seq;      // -1: the row belongs to no sequence
+  int64_t pos;  // may be negative
+};
+
+__device__ __forceinline__ RowAt row_at(const DecodeRows& r, int t) {
+  if (!r.row_start) return {t, (int64_t)r.kv_len[t] - 1};
+  const int b = seq_of_row(r.row_start, r.n_seqs, t);
+  if (b >= r.n_seqs || t < r.row_start[b]) return {-1, 0};
+  return {b, (int64_t)r.kv_len[b] - r.row_start[b + 1] + t};
+}
+
+// cos and sin of pos * 10000^(-2 i / 64).  The angle is taken in turns in double precision and reduced
+// there (2^31 positions: error below 1e-6 of a turn), so that far positions keep fp32 accuracy.
+__device__ __forceinline__ void rope_angle(int64_t pos, int i, float* cs, float* sn) {
+  const double turns = (double)pos * (exp2(-(double)i * (13.287712379549449 / (kLatRope / 2))) * 0.15915494309189535);
+  sincospif(2.f * (float)(turns - rint(turns)), sn, cs);
+}
+
+// ------------------------------------------------------------------------------------ KDA step
+struct StepArgs {
+  const void *q, *k, *v, *g, *beta;
+  float* state;
+  const int32_t *src, *dst;  // dst NULL: in place
+  void* o;
+  int n_slots, H;
+  DecodeRows rows;
+  int* status;
+};
+
+// N consecutive elements (N * sizeof(T) a power of two up to 32 bytes, aligned to min(that, 16))
+template <typename T, int N>
+__device__ __forceinline__ void load_vec(const T* p, float (&x)[N]) {
+  constexpr int B = N * (int)sizeof(T);
+  if constexpr (B >= 16) {
+    constexpr int V = 16 / sizeof(T);
+#pragma unroll
+    for (int j = 0; j < N / V; ++j) {
+      const uint4 u = reinterpret_cast<const uint4*>(p)[j];
+      const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[j * V + i] = to_f(e[i]);
+    }
+  } else if constexpr (B == 8) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_f(e[i]);
+  } else {
+    static_assert(B == 4, "vector width");
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_f(e[i]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float (&x)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+    __align__(8) T e[4] = {from_f<T>(x[0]), from_f<T>(x[1]), from_f<T>(x[2]), from_f<T>(x[3])};
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+  }
+}
+
+constexpr int kStepThreads = 128;
+
+// The columns of S evolve independently: with Sd = Diag(e^g) S, u = Sd^T k and w = Sd^T q,
+//   delta = beta (v - u),  S' = Sd + k delta^T,  o = S'^T q = w + (k . q) delta,
+// so one pass over a column does everything.  A warp owns 8 columns of one head's state in
+// registers: lane = (16 groups of D / 16 rows) x (2 groups of 4 columns), sums over the rows are
+// shuffles, and nothing is shared between warps (no barrier).  Every 16-byte load takes half a
+// 32-byte sector and its neighbour lane the other half.
+template <typename T, typename TO, int D>
+__global__ void __launch_bounds__(kStepThreads) kda_step_kernel(StepArgs a) {
+  constexpr int R = D / 16, SL = D / 8;  // rows per lane, warps per head
+  const int lane = threadIdx.x & 31, rg = lane >> 1;
+  const int64_t unit = (int64_t)blockIdx.x * (kStepThreads / 32) + (threadIdx.x >> 5);
+  const int64_t bh = unit / SL;
+  const int sl = (int)(unit % SL), h = (int)(bh % a.H);
+  const int64_t b64 = bh / a.H;
+  if (b64 >= a.rows.n_seqs) return;
+  const int b = (int)b64;
+  const int src = a.src[b], dst = a.dst ? a.dst[b] : src;
+  const int t0 = a.rows.row_start ? a.rows.row_start[b] : b, t1 = a.rows.row_start ? a.rows.row_start[b + 1] : b + 1;
+  if (src < 0) return;  // padding entry
+  if (src >= a.n_slots || dst < 0 || dst >= a.n_slots || t0 < 0 || t1 < t0 || t1 > a.rows.n_rows) {
+    if (lane == 0) set_status(a.status, kStatusCheck);
+    return;
+  }
+  // one warp per sequence looks for another sequence that writes or reads the slot it writes
+  if (a.status && h == 0 && sl == 0) {
+    bool clash = false;
+    for (int j = lane; j < a.rows.n_seqs; j += 32) {
+      const int sj = a.src[j];
+      if (j == b || sj < 0) continue;
+      clash |= sj == dst || (a.dst && a.dst[j] == dst);
+    }
+    if (__any_sync(0xffffffffu, clash) && lane == 0) set_status(a.status, kStatusCheck);
+  }
+  const int r0 = rg * R, c0 = sl * 8 + (lane & 1) * 4;
+  const size_t at = (size_t)r0 * D + c0;
+  const float* sp = a.state + ((size_t)src * a.H + h) * D * D + at;
+  float S[R][4];
+#pragma unroll
+  for (int i = 0; i < R; ++i) load_vec<float, 4>(sp + (size_t)i * D, S[i]);
+  for (int t = t0; t < t1; ++t) {
+    const size_t row = ((size_t)t * a.H + h) * D;
+    float q[R], k[R], g[R], v[4];
+    load_vec<T, R>((const T*)a.q + row + r0, q);
+    load_vec<T, R>((const T*)a.k + row + r0, k);
+    load_vec<T, R>((const T*)a.g + row + r0, g);
+    load_vec<T, 4>((const T*)a.v + row + c0, v);
+    const float beta = to_f(((const T*)a.beta)[(size_t)t * a.H + h]);
+    float u[4] = {}, w[4] = {}, kq = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float al = expf(g[i]);
+      kq = fmaf(k[i], q[i], kq);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        S[i][j] *= al;
+        u[j] = fmaf(S[i][j], k[i], u[j]);
+        w[j] = fmaf(S[i][j], q[i], w[j]);
+      }
+    }
+#pragma unroll
+    for (int m = 2; m < 32; m <<= 1) {
+      kq += __shfl_xor_sync(0xffffffffu, kq, m);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u[j] += __shfl_xor_sync(0xffffffffu, u[j], m);
+        w[j] += __shfl_xor_sync(0xffffffffu, w[j], m);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u[j] = beta * (v[j] - u[j]);
+      w[j] = fmaf(kq, u[j], w[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) S[i][j] = fmaf(k[i], u[j], S[i][j]);
+    if (rg == 0) store4((TO*)a.o + row + c0, w);
+  }
+  float* dp = a.state + ((size_t)dst * a.H + h) * D * D + at;
+#pragma unroll
+  for (int i = 0; i < R; ++i) store4(dp + (size_t)i * D, S[i]);
+}
+
+// ------------------------------------------------------------------------------------ cache append
+struct AppendArgs {
+  LatentCache cache;
+  DecodeRows rows;
+  const void *c, *kr;
+  int64_t ld_c, ld_kr;
+  int* status;
+};
+
+constexpr int kAppendThreads = 128;
+
+// One warp per row: 16 latent elements per lane, then lane i turns the pair (i, i + 32) of the
+// rotary key.  Bound by the row's bytes; each is read and written once.
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t64 = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  if (t64 >= a.rows.n_rows) return;
+  const int t = (int)t64;
+  const RowAt r = row_at(a.rows, t);
+  if (r.seq < 0 || r.pos < 0) return;
+  const int64_t pg = r.pos / a.cache.page_size;
+  const int page = pg < a.cache.max_pages ? a.cache.table[(size_t)r.seq * a.cache.max_pages + pg] : -1;
+  if (page < 0 || page >= a.cache.n_pages) {
+    if (lane == 0) set_status(a.status, kStatusCheck);
+    return;
+  }
+  __nv_bfloat16* dst =
+      a.cache.data + ((size_t)page * a.cache.page_size + (size_t)(r.pos - pg * a.cache.page_size)) * kLatWidth;
+  const T* c = (const T*)a.c + (size_t)t * a.ld_c;
+  const T* kr = (const T*)a.kr + (size_t)t * a.ld_kr;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float x[8];
+    load_vec<T, 8>(c + (j * 32 + lane) * 8, x);
+    __align__(16) __nv_bfloat16 e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = __float2bfloat16_rn(x[i]);
+    reinterpret_cast<uint4*>(dst)[j * 32 + lane] = *reinterpret_cast<const uint4*>(e);
+  }
+  const float x = to_f(kr[lane]), y = to_f(kr[lane + 32]);
+  float cs, sn;
+  rope_angle(r.pos, lane, &cs, &sn);
+  dst[kLatDim + lane] = __float2bfloat16_rn(x * cs - y * sn);
+  dst[kLatDim + 32 + lane] = __float2bfloat16_rn(x * sn + y * cs);
+  // a page that two sequences both write: the first of this row's run in the page compares the
+  // (sequence, page) pairs of the batch
+  if (!a.status) return;
+  const int first = a.rows.row_start ? a.rows.row_start[r.seq] : t;
+  if (t != first && r.pos % a.cache.page_size) return;
+  bool clash = false;
+  for (int s = 0; s < a.rows.n_seqs; ++s) {
+    const int m = a.rows.row_start ? a.rows.row_start[s + 1] - a.rows.row_start[s] : 1;
+    const int64_t kv = a.rows.kv_len[s], p0 = max((int64_t)0, kv - m) / a.cache.page_size;
+    const int64_t p1 = min((kv + a.cache.page_size - 1) / a.cache.page_size, (int64_t)a.cache.max_pages);
+    if (m <= 0) continue;
+    for (int64_t p = p0 + lane; p < p1; p += 32)
+      clash |= !(s == r.seq && p == pg) && a.cache.table[(size_t)s * a.cache.max_pages + p] == page;
+  }
+  if (__any_sync(0xffffffffu, clash) && lane == 0) set_status(a.status, kStatusCheck);
+}
+
+// ------------------------------------------------------------------------------------ rotated queries
+// The rotary part of the absorbed queries: a warp turns every head of one row (lane i: the pair i, i + 32).
+__device__ __forceinline__ void absorb_rope_row(const DecodeRows& rows, int H, const __nv_bfloat16* q, int64_t ld_q,
+                                                __nv_bfloat16* qa, int t) {
+  const int lane = threadIdx.x & 31;
+  const RowAt r = row_at(rows, t);
+  if (r.seq < 0) return;
+  float cs, sn;
+  rope_angle(r.pos, lane, &cs, &sn);
+  for (int h = 0; h < H; ++h) {
+    const __nv_bfloat16* s = q + (size_t)t * ld_q + (size_t)h * kLatQK + kLatHead;
+    __nv_bfloat16* d = qa + ((size_t)t * H + h) * kLatWidth + kLatDim;
+    const float x = to_f(s[lane]), y = to_f(s[lane + 32]);
+    d[lane] = __float2bfloat16_rn(x * cs - y * sn);
+    d[lane + 32] = __float2bfloat16_rn(x * sn + y * cs);
+  }
+}
+
+constexpr int kHeadThreads = 128;
+
+// One CTA per (row, head): 512 dot products of 128 terms, thread = 4 neighbouring outputs.
+__global__ void __launch_bounds__(kHeadThreads)
+    latent_absorb_kernel(DecodeRows rows, int H, const __nv_bfloat16* q, int64_t ld_q, const __nv_bfloat16* w_b,
+                         __nv_bfloat16* qa) {
+  __shared__ float x[kLatHead];
+  const int t = (int)(blockIdx.x / H), h = (int)(blockIdx.x % H);
+  if (rows.row_start && (t >= rows.row_start[rows.n_seqs] || t < rows.row_start[0])) return;
+  if (h == 0 && threadIdx.x < 32) absorb_rope_row(rows, H, q, ld_q, qa, t);
+  x[threadIdx.x] = to_f(q[(size_t)t * ld_q + (size_t)h * kLatQK + threadIdx.x]);
+  __syncthreads();
+  float acc[4] = {};
+  const __nv_bfloat16* w = w_b + (size_t)h * kLatHead * kLatDim + 4 * threadIdx.x;
+  for (int i = 0; i < kLatHead; ++i) {
+    float y[4];
+    load_vec<__nv_bfloat16, 4>(w + (size_t)i * kLatDim, y);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = fmaf(x[i], y[j], acc[j]);
+  }
+  store4(qa + ((size_t)t * H + h) * kLatWidth + 4 * threadIdx.x, acc);
+}
+
+// One CTA per (row, head): 128 dot products of 512 terms, thread = output.
+__global__ void __launch_bounds__(kHeadThreads)
+    latent_expand_kernel(int H, const __nv_bfloat16* o, const __nv_bfloat16* w_b, __nv_bfloat16* out) {
+  __shared__ float x[kLatDim];
+  const int t = (int)(blockIdx.x / H), h = (int)(blockIdx.x % H);
+  float y[8];
+  load_vec<__nv_bfloat16, 4>(o + ((size_t)t * H + h) * kLatDim + 4 * threadIdx.x, *reinterpret_cast<float(*)[4]>(y));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[4 * threadIdx.x + j] = y[j];
+  __syncthreads();
+  const __nv_bfloat16* w = w_b + ((size_t)(H + h) * kLatHead + threadIdx.x) * kLatDim;
+  float acc = 0.f;
+  for (int i = 0; i < kLatDim; i += 8) {
+    load_vec<__nv_bfloat16, 8>(w + i, y);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc = fmaf(x[i + j], y[j], acc);
+  }
+  out[((size_t)t * H + h) * kLatHead + threadIdx.x] = __float2bfloat16_rn(acc);
+}
+
+// One CTA per (row, head): softmax attention over the row's cached tokens, 128 at a time: thread =
+// token for the scores, thread = 4 latent dimensions for the weighted sum.
+__global__ void __launch_bounds__(kHeadThreads)
+    latent_attn_kernel(LatentCache cache, DecodeRows rows, int H, float scale, const __nv_bfloat16* qa,
+                       __nv_bfloat16* o, float* lse, int* status) {
+  __shared__ float q[kLatWidth], p[kHeadThreads], red[4];
+  __shared__ size_t at[kHeadThreads];
+  const int tid = threadIdx.x, t = (int)(blockIdx.x / H), h = (int)(blockIdx.x % H);
+  const RowAt r = row_at(rows, t);
+  if (r.seq < 0) return;
+  const size_t row = (size_t)t * H + h;
+  for (int i = tid; i < kLatWidth; i += kHeadThreads) q[i] = to_f(qa[row * kLatWidth + i]);
+  int64_t n = r.pos + 1;
+  if (rows.kv_len[r.seq] > (int64_t)cache.max_pages * cache.page_size) {
+    if (tid == 0) set_status(status, kStatusCheck);
+    n = min(n, (int64_t)cache.max_pages * cache.page_size);
+  }
+  float mx = -INFINITY, sum = 0.f, acc[4] = {};
+  for (int64_t j0 = 0; j0 < n; j0 += kHeadThreads) {
+    __syncthreads();
+    float s = -INFINITY;
+    if (j0 + tid < n) {
+      const int64_t pg = (j0 + tid) / cache.page_size;
+      int page = cache.table[(size_t)r.seq * cache.max_pages + pg];
+      if (page < 0 || page >= cache.n_pages) {
+        set_status(status, kStatusCheck);
+        page = 0;
+      }
+      at[tid] = ((size_t)page * cache.page_size + (size_t)(j0 + tid - pg * cache.page_size)) * kLatWidth;
+      s = 0.f;
+      for (int i = 0; i < kLatWidth; i += 8) {
+        float x[8];
+        load_vec<__nv_bfloat16, 8>(cache.data + at[tid] + i, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(q[i + e], x[e], s);
+      }
+      s *= scale;
+    }
+    float m = s;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((tid & 31) == 0) red[tid >> 5] = m;
+    __syncthreads();
+    m = fmaxf(mx, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
+    const float base = m == -INFINITY ? 0.f : m, f = expf(mx - base);
+    mx = m;
+    p[tid] = expf(s - base);
+    __syncthreads();
+    sum *= f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] *= f;
+    const int nn = (int)min((int64_t)kHeadThreads, n - j0);
+    for (int j = 0; j < nn; ++j) {
+      float x[4];
+      load_vec<__nv_bfloat16, 4>(cache.data + at[j] + 4 * tid, x);
+      sum += p[j];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(p[j], x[e], acc[e]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] *= inv;
+  store4(o + row * kLatDim + 4 * tid, acc);
+  if (tid == 0) lse[row] = mx + logf(sum);
+}
+
+}  // namespace tpc
