@@ -8,10 +8,13 @@
 #include "../../include/tpc.h"
 #include "abi_internal.h"
 #include "decode_kernels.cuh"
+#include "latent_tc.cuh"
 
 namespace {
 using tpc_abi::fail;
 using tpc_abi::g_prof;
+using tpc_abi::set_smem;
+using tpc_abi::tensor_map;
 using bf = __nv_bfloat16;
 
 static_assert(TPC_LATENT_DIM == tpc::kLatDim && TPC_LATENT_ROPE == tpc::kLatRope && TPC_LATENT_HEAD == tpc::kLatHead &&
@@ -132,7 +135,7 @@ int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld
   return TPC_OK;
 }
 
-size_t tpc_latent_attn_scratch_bytes(int32_t H) { return H < 1 || H > kLatMaxH ? 0 : 256; }
+size_t tpc_latent_attn_scratch_bytes(int32_t H) { return H < 1 || H > kLatMaxH ? 0 : tpc::kLatScratch; }
 
 int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t H, float scale, const void* qa,
                     void* o, float* lse, void* scratch, size_t scratch_bytes, int32_t* status, tpc_stream_t stream) {
@@ -148,10 +151,28 @@ int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t
     return fail(TPC_ERR_WORKSPACE, "latent attention: scratch too small or not 256-byte aligned");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   tpc_abi::NvtxRange nvtx_call("tpc_latent_attn");
-  const unsigned grid = (unsigned)((int64_t)r.n_rows * H);
-  TPC_LAUNCH("latent_attn", st, (tpc::latent_attn_kernel<<<grid, tpc::kHeadThreads, 0, st>>>(
-                                    lc, r, H, scale, (const bf*)qa, (bf*)o, lse, status)));
-  return TPC_OK;
+  CUtensorMap tkv, tq;
+  // columns of a tile: the (row, head) pairs that an average sequence has
+  const int64_t cols = ((int64_t)r.n_rows * H + r.n_seqs - 1) / r.n_seqs;
+  const int NT = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
+  if (!tensor_map(&tkv, lc.data, tpc::kLatWidth, (uint64_t)lc.n_pages * lc.page_size, tpc::kLatWidth, std::min(lc.page_size, tpc::kLatKT)) ||
+      !tensor_map(&tq, qa, tpc::kLatWidth, (uint64_t)r.n_rows * H, tpc::kLatWidth, NT))
+    return fail(TPC_ERR_CUDA, "latent attention: cuTensorMapEncodeTiled failed");
+  char* sc = static_cast<char*>(scratch);
+  const tpc::LatAttnArgs a{lc, r, H, scale * 1.4426950408889634f, (bf*)o, lse, (float*)sc, (float2*)(sc + tpc::kLatPartBytes),
+                           (tpc::LatPiece*)(sc + tpc::kLatPartBytes + tpc::kLatMlBytes), status, 1};
+  const int grid = std::min(tpc_abi::sm_count(), tpc::kLatMaxCtas);
+  auto go = [&](auto nt) -> int {
+    constexpr int N = decltype(nt)::value;
+    constexpr size_t smem = tpc::LatSmem<N>::total;
+    TPC_CUDA(set_smem(tpc::latent_attn_tc<N>, smem));
+    TPC_LAUNCH("latent_attn_tc", st, (tpc::latent_attn_tc<N><<<grid, tpc::kLatAttnThreads, smem, st>>>(tkv, tq, a)));
+    TPC_LAUNCH("latent_combine", st, (tpc::latent_combine_kernel<<<dim3(grid, N), 128, 0, st>>>(a)));
+    return TPC_OK;
+  };
+  if (NT == 16) return go(std::integral_constant<int, 16>{});
+  if (NT == 32) return go(std::integral_constant<int, 32>{});
+  return go(std::integral_constant<int, 64>{});
 }
 
 int tpc_latent_expand(int32_t n_rows, int32_t H, const void* o, const void* w_b, void* out, int32_t* status,

@@ -1,5 +1,5 @@
 // Kernels of token-by-token generation: the recurrent KDA step on a cache of states, the append to
-// the paged cache of latents, and the simple forms of latent attention and its per-head products.
+// the paged cache of latents, and the per-head products of latent attention.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -315,73 +315,6 @@ __global__ void __launch_bounds__(kHeadThreads)
     for (int j = 0; j < 8; ++j) acc = fmaf(x[i + j], y[j], acc);
   }
   out[((size_t)t * H + h) * kLatHead + threadIdx.x] = __float2bfloat16_rn(acc);
-}
-
-// One CTA per (row, head): softmax attention over the row's cached tokens, 128 at a time: thread =
-// token for the scores, thread = 4 latent dimensions for the weighted sum.
-__global__ void __launch_bounds__(kHeadThreads)
-    latent_attn_kernel(LatentCache cache, DecodeRows rows, int H, float scale, const __nv_bfloat16* qa,
-                       __nv_bfloat16* o, float* lse, int* status) {
-  __shared__ float q[kLatWidth], p[kHeadThreads], red[4];
-  __shared__ size_t at[kHeadThreads];
-  const int tid = threadIdx.x, t = (int)(blockIdx.x / H), h = (int)(blockIdx.x % H);
-  const RowAt r = row_at(rows, t);
-  if (r.seq < 0) return;
-  const size_t row = (size_t)t * H + h;
-  for (int i = tid; i < kLatWidth; i += kHeadThreads) q[i] = to_f(qa[row * kLatWidth + i]);
-  int64_t n = r.pos + 1;
-  if (rows.kv_len[r.seq] > (int64_t)cache.max_pages * cache.page_size) {
-    if (tid == 0) set_status(status, kStatusCheck);
-    n = min(n, (int64_t)cache.max_pages * cache.page_size);
-  }
-  float mx = -INFINITY, sum = 0.f, acc[4] = {};
-  for (int64_t j0 = 0; j0 < n; j0 += kHeadThreads) {
-    __syncthreads();
-    float s = -INFINITY;
-    if (j0 + tid < n) {
-      const int64_t pg = (j0 + tid) / cache.page_size;
-      int page = cache.table[(size_t)r.seq * cache.max_pages + pg];
-      if (page < 0 || page >= cache.n_pages) {
-        set_status(status, kStatusCheck);
-        page = 0;
-      }
-      at[tid] = ((size_t)page * cache.page_size + (size_t)(j0 + tid - pg * cache.page_size)) * kLatWidth;
-      s = 0.f;
-      for (int i = 0; i < kLatWidth; i += 8) {
-        float x[8];
-        load_vec<__nv_bfloat16, 8>(cache.data + at[tid] + i, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(q[i + e], x[e], s);
-      }
-      s *= scale;
-    }
-    float m = s;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if ((tid & 31) == 0) red[tid >> 5] = m;
-    __syncthreads();
-    m = fmaxf(mx, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float base = m == -INFINITY ? 0.f : m, f = expf(mx - base);
-    mx = m;
-    p[tid] = expf(s - base);
-    __syncthreads();
-    sum *= f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] *= f;
-    const int nn = (int)min((int64_t)kHeadThreads, n - j0);
-    for (int j = 0; j < nn; ++j) {
-      float x[4];
-      load_vec<__nv_bfloat16, 4>(cache.data + at[j] + 4 * tid, x);
-      sum += p[j];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = fmaf(p[j], x[e], acc[e]);
-    }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) acc[e] *= inv;
-  store4(o + row * kLatDim + 4 * tid, acc);
-  if (tid == 0) lse[row] = mx + logf(sum);
 }
 
 }  // namespace tpc

@@ -1,0 +1,592 @@
+// Absorbed latent attention over a paged cache on 5th-generation tensor cores (sm_100a).
+//
+// Every head of every new row of a sequence reads the same cached rows [c | kr], so the (row, head)
+// pairs of a sequence are the columns of one product with the cache as its tall operand:
+//   S^T [64 tokens x NT columns] = K [64 x 576] Qa^T,   O^T [512 x NT] += C^T [512 x 64] P^T [64 x NT].
+// The cached tile is the MMA's A operand both times, once K-major and once (its latent part, the same
+// shared memory) MN-major, and is fetched once; the few columns are N, which the tensor core takes
+// in steps of 16 (rows as M would fill 16 of 128 lanes).
+#pragma once
+#include <cuda.h>
+
+#include "common.cuh"
+#include "decode_kernels.cuh"
+#include "tc.cuh"
+
+namespace tpc {
+
+constexpr int kLatKT = 64;                          // tokens per tile
+constexpr int kLatChunks = kLatWidth / 64;          // 64-column boxes of a cached row (the last one rotary)
+constexpr int kLatAttnThreads = 192;                // producer warp, MMA warp, four softmax warps
+constexpr int kLatMaxCtas = 148;
+constexpr int kLatMaxNT = 64;
+constexpr uint32_t kLatStage = kLatChunks * kLatKT * 128;
+
+template <int NT>
+struct LatSmem {
+  static constexpr uint32_t PB = NT == 64 ? 1 : 2, RB = PB;  // buffers of P and of the maxima
+  static constexpr uint32_t q = 0, stage = q + kLatChunks * NT * 128, p = stage + 2 * kLatStage, end = p + PB * NT * 128;
+  static constexpr uint32_t red = end, fac = red + RB * 4 * NT * 4, lim = fac + NT * 4, bars = lim + NT * 4;
+  static constexpr uint32_t total = bars + 256 + 1024;  // + slack to align the tiles to 1024 bytes
+};
+static_assert(LatSmem<64>::total <= 232448, "shared memory of one CTA");
+
+// scratch: partial sums of the pieces (two per CTA), their (max, sum), and one record per CTA
+struct LatPiece {
+  long long col0;  // first (row, head) pair of the split unit that starts in this CTA
+  int ncols;
+  int n;           // its pieces: this CTA's last one, then the first ones of the next n - 1 CTAs
+};
+constexpr size_t kLatPartBytes = (size_t)kLatMaxCtas * 2 * kLatMaxNT * kLatDim * 4;
+constexpr size_t kLatMlBytes = (size_t)kLatMaxCtas * 2 * kLatMaxNT * 8;
+constexpr size_t kLatScratch = kLatPartBytes + kLatMlBytes + ((kLatMaxCtas * sizeof(LatPiece) + 255) / 256) * 256;
+
+struct LatAttnArgs {
+  LatentCache cache;
+  DecodeRows rows;
+  int H;
+  float scale_log2;  // scale * log2(e)
+  __nv_bfloat16* o;
+  float* lse;
+  float* part;
+  float2* ml;
+  LatPiece* meta;
+  int* status;
+  int min_tiles;
+};
+
+struct LatSeq {
+  int row0, m, kv;
+};
+
+__device__ __forceinline__ LatSeq lat_seq(const LatAttnArgs& a, int b) {
+  LatSeq s;
+  s.row0 = a.rows.row_start ? a.rows.row_start[b] : b;
+  const int end = a.rows.row_start ? a.rows.row_start[b + 1] : b + 1;
+  s.m = end - s.row0;
+  if (s.row0 < 0 || end < s.row0 || end > a.rows.n_rows) {
+    set_status(a.status, kStatusCheck);
+    s.row0 = s.m = 0;
+  }
+  s.kv = max(a.rows.kv_len[b], 0);
+  const int cap = a.cache.max_pages * a.cache.page_size;
+  if (s.kv > cap && s.m > 0) set_status(a.status, kStatusCheck);
+  s.kv = min(s.kv, cap);
+  return s;
+}
+
+// column tiles of a sequence
+template <int NT>
+__device__ __forceinline__ int lat_cts(const LatAttnArgs& a, const LatSeq& s) {
+  return (int)(((long long)s.m * a.H + NT - 1) / NT);
+}
+// token tiles that the columns of column tile ct can see (at least one: the rows are written either way)
+template <int NT>
+__device__ __forceinline__ int lat_tiles(const LatAttnArgs& a, const LatSeq& s, int ct) {
+  const int last = min((int)(((long long)(ct + 1) * NT - 1) / a.H), s.m - 1);
+  return max(1, (s.kv - s.m + last + kLatKT) / kLatKT);
+}
+
+// Walks a CTA's share of the work: pieces (column tile of a sequence, range of token tiles)
+template <int NT>
+struct LatWalk {
+  const LatAttnArgs& a;
+  long long left;
+  int b, ct, t0, n, tiles;
+  LatSeq s;
+  __device__ LatWalk(const LatAttnArgs& args, int b0, int ct0, int tile0, long long count)
+      : a(args), left(count), b(b0), ct(ct0), t0(tile0), n(0), tiles(0) {
+    if (left > 0) enter();
+  }
+  __device__ void enter() {
+    s = lat_seq(a, b);
+    size();
+  }
+  __device__ void size() {
+    tiles = lat_tiles<NT>(a, s, ct);
+    n = (int)min((long long)(tiles - t0), left);
+  }
+  __device__ void next() {  // the share's weights were summed from the same numbers, so b stays in range
+    left -= n;
+    if (left <= 0) return;
+    t0 = 0;
+    if (++ct < lat_cts<NT>(a, s)) {
+      size();
+      return;
+    }
+    ct = 0;
+    do {
+      if (++b >= a.rows.n_seqs) {
+        left = 0;
+        return;
+      }
+      s = lat_seq(a, b);
+    } while (s.m <= 0);
+    size();
+  }
+};
+
+// 8 * R columns of 16 TMEM lanes, spread over the warp: x[4 j + e] is lane l / 4 + 8 (e / 2), column
+// 8 j + 2 (l % 4) + e % 2
+template <int R>
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&x)[4 * R]) {
+  uint32_t r[4 * R];
+  if constexpr (R == 2) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  } else if constexpr (R == 4) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  } else {
+    static_assert(R == 8, "16, 32 or 64 columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+  }
+  tc::tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 4 * R; ++i) {
+    asm volatile("" : "+r"(r[i]));
+    x[i] = __uint_as_float(r[i]);
+  }
+}
+
+// four 8 x 8 bf16 matrices in MMA accumulator order, each stored transposed: lane l gives the address of
+// stored row l % 8 (16 bytes) of matrix l / 8
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Persistent: the token tiles of all (sequence, column tile) units are one list, cut into equal
+// shares, one CTA each, so ragged lengths balance and one long context uses every SM.  The shares are
+// found on the device from kv_len (no host copy, graphs replay with new lengths).  A unit that is cut
+// leaves partial sums for latent_combine_kernel.
+//
+// Warp 0 fetches tiles by TMA (64-column boxes, one per page and column chunk) into two stages, warp 1
+// issues the MMAs, warps 2-5 run the softmax: a warp holds 16 tokens x NT columns of S^T in the
+// 16x256b register layout (all lanes busy although M = 64 fills half the TMEM lanes), maxima over
+// tokens are 3 shuffles and one exchange between the four warps.  Running sums stay per lane until
+// the piece ends.  The maximum is only raised when it grew by more than 8 (base 2): until then the
+// weights are at most 2^8 and the sums of the old maximum stay valid, which saves the pass over O^T.
+// S of tile i + 1 runs on the tensor core while tile i is in the softmax.
+template <int NT>
+__global__ void __launch_bounds__(kLatAttnThreads, 1)
+    latent_attn_tc(const __grid_constant__ CUtensorMap tma_kv, const __grid_constant__ CUtensorMap tma_q, LatAttnArgs a) {
+  using namespace tc;
+  using L = LatSmem<NT>;
+  constexpr int R = NT / 8;
+  extern __shared__ __align__(1024) uint8_t lsm_raw[];
+  uint8_t* sm = lsm_raw + ((1024u - (smem_u32(lsm_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(sm);
+  float* red = reinterpret_cast<float*>(sm + L::red);
+  float* fac = reinterpret_cast<float*>(sm + L::fac);
+  int* lim = reinterpret_cast<int*>(sm + L::lim);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
+  uint64_t *full = bars, *empty = bars + 2, *s_full = bars + 4, *p_full = bars + 6, *o_done = bars + 8, *q_full = bars + 10,
+           *q_empty = bars + 11, *done = bars + 12;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 13);
+  int* abort_flag = reinterpret_cast<int*>(bars + 13) + 1;
+  int* where = reinterpret_cast<int*>(bars + 14);               // b, ct, tile of the share's start
+  long long* sums = reinterpret_cast<long long*>(bars + 16);    // per warp
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+
+  // ---- this CTA's share
+  const int lo = (int)((long long)a.rows.n_seqs * tid / kLatAttnThreads);
+  const int hi = (int)((long long)a.rows.n_seqs * (tid + 1) / kLatAttnThreads);
+  long long mine = 0;
+  for (int b = lo; b < hi; ++b) {
+    const LatSeq s = lat_seq(a, b);
+    const int n = lat_cts<NT>(a, s);
+    for (int c = 0; c < n; ++c) mine += lat_tiles<NT>(a, s, c);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) sums[w] = incl;
+  if (w == 1) tmem_alloc(tslot, NT == 16 ? 128 : NT == 32 ? 256 : 512);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
+    }
+    for (uint64_t* b : {q_full, q_empty, done}) mbar_init(b, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  long long total = 0;
+  for (int i = 0; i < kLatAttnThreads / 32; ++i) {
+    if (i < w) incl += sums[i];
+    total += sums[i];
+  }
+  const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)a.min_tiles);
+  const long long start = per * blockIdx.x, share = max(0ll, min(per, total - start));
+  if (share > 0 && start >= incl - mine && start < incl) {
+    long long at = start - (incl - mine);
+    for (int b = lo; b < hi; ++b) {
+      const LatSeq s = lat_seq(a, b);
+      const int n = lat_cts<NT>(a, s);
+      for (int c = 0; c < n; ++c) {
+        const int t = lat_tiles<NT>(a, s, c);
+        if (at >= 0 && at < t) {
+          where[0] = b;
+          where[1] = c;
+          where[2] = (int)at;
+        }
+        at -= t;
+      }
+    }
+  }
+  __syncthreads();
+  const uint32_t tb = *tslot;
+  LatWalk<NT> walk(a, where[0], where[1], where[2], share);
+  auto aborted = [&] { return *((volatile int*)abort_flag) != 0; };
+  // Every wait is bounded.  After the first that runs out no role waits, copies or multiplies any
+  // more, but all walk on to the end of their loops, so the barriers between the softmax warps match.
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (aborted()) return false;
+    if (mbar_wait(bar, parity, 2000000000ull)) return true;
+    set_status(a.status, 8);
+    atomicExch(abort_flag, 1);
+    return false;
+  };
+
+  if (w == 0) {  // ---- producer
+    const int ps = a.cache.page_size, box = min(ps, kLatKT);
+    int it = 0, piece = 0;
+    for (; walk.left > 0; walk.next(), ++piece) {
+      const LatSeq s = walk.s;
+      const int32_t* table = a.cache.table + (size_t)walk.b * a.cache.max_pages;
+      bool ok = piece == 0 || wait(q_empty, (piece - 1) & 1);
+      if (lane == 0 && ok) {
+        mbar_arrive_expect_tx(q_full, kLatChunks * NT * 128);
+        for (int c = 0; c < kLatChunks; ++c)
+          tma_load_2d(sm + L::q + c * NT * 128, &tma_q, 64 * c, s.row0 * a.H + walk.ct * NT, q_full);
+      }
+      for (int i = 0; i < walk.n; ++i, ++it) {
+        const int t0 = (walk.t0 + i) * kLatKT, st = it & 1;
+        const int segs = (min(max(s.kv - t0, 0), kLatKT) + box - 1) / box;
+        // this lane's boxes: (segment, chunk) pairs lane and lane + 32; their pages are read before the wait
+        int row[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = lane + 32 * e, tok = t0 + j / kLatChunks * box;
+          row[e] = 0;
+          if (j < segs * kLatChunks) {
+            int page = table[tok / ps];
+            if (page < 0 || page >= a.cache.n_pages) {
+              set_status(a.status, kStatusCheck);
+              page = 0;
+            }
+            row[e] = page * ps + tok % ps;
+          }
+        }
+        ok = it < 2 || wait(&empty[st], ((it >> 1) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        if (lane == 0) {
+          if (segs)
+            mbar_arrive_expect_tx(&full[st], segs * kLatChunks * box * 128);
+          else
+            mbar_arrive(&full[st]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = lane + 32 * e, seg = j / kLatChunks, c = j % kLatChunks;
+          if (j < segs * kLatChunks)
+            tma_load_2d(sm + L::stage + st * kLatStage + (c * kLatKT + seg * box) * 128, &tma_kv, 64 * c, row[e], &full[st]);
+        }
+      }
+    }
+    if (aborted() && lane == 0) {  // copies in flight land before the CTA ends
+      for (int i = max(0, it - 2); i < it; ++i) mbar_wait(&full[i & 1], (i >> 1) & 1, 100000000ull);
+      mbar_wait(q_full, (piece - 1) & 1, 100000000ull);
+    }
+  } else if (w == 1) {  // ---- MMA
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16(64, NT, false, false), id_o = idesc_bf16(128, NT, true, false);
+      int it = 0, piece = 0;
+      auto weighted_sum = [&](int i, bool first) {  // O^T (+)= C^T P^T of tile i
+        if (!wait(&p_full[i & 1], (i >> 1) & 1)) return;
+        fence_after_sync();
+        const uint32_t kv = sb + L::stage + (i & 1) * kLatStage, p = sb + L::p + (i % L::PB) * NT * 128;
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+          for (int ks = 0; ks < kLatKT / 16; ++ks)
+            mma_bf16(tb + mb * NT, sw_desc_mn(kv + 2 * mb * kLatKT * 128, kLatKT, ks), sw_desc_k(p, NT, ks), id_o,
+                     first && ks == 0 ? 0u : 1u);
+        commit(&o_done[i & 1]);
+        commit(&empty[i & 1]);
+      };
+      for (; walk.left > 0; walk.next(), ++piece) {
+        wait(q_full, piece & 1);
+        for (int i = 0; i < walk.n; ++i, ++it) {
+          if (wait(&full[it & 1], (it >> 1) & 1)) {
+            fence_after_sync();
+            const uint32_t kv = sb + L::stage + (it & 1) * kLatStage;
+#pragma unroll 4
+            for (int ks = 0; ks < kLatWidth / 16; ++ks)
+              mma_bf16(tb + 4 * NT + (it & 1) * NT, sw_desc_k(kv, kLatKT, ks), sw_desc_k(sb + L::q, NT, ks), id_s, ks ? 1u : 0u);
+            commit(&s_full[it & 1]);
+            if (i == walk.n - 1) commit(q_empty);
+          }
+          if (i > 0) weighted_sum(it - 1, i == 1);
+        }
+        weighted_sum(it - 1, walk.n == 1);
+      }
+      commit(done);
+      if (!mbar_wait(done, 0, 2000000000ull)) set_status(a.status, 8);
+    }
+  } else {  // ---- softmax warps: sub-partition sp holds tokens 16 sp .. 16 sp + 15 of a tile, and
+            //      latent dimensions 32 sp .. 32 sp + 31 of each 128-row block of O^T
+    const int sp = w & 3, k0 = 16 * sp + (lane >> 2), st = tid - 64;
+    const uint32_t la = tb + ((uint32_t)(32 * sp) << 16);
+    auto meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    int it = 0;
+    if (st == 0 && share > 0) a.meta[blockIdx.x].n = 0;
+    for (; walk.left > 0; walk.next()) {
+      const LatSeq s = walk.s;
+      const long long col0 = (long long)s.row0 * a.H + (long long)walk.ct * NT;
+      const int ncols = (int)min((long long)NT, (long long)s.m * a.H - (long long)walk.ct * NT);
+      // last visible position of every column (columns past the run's end take its last row's)
+      if (st < NT) lim[st] = s.kv - s.m + min((int)(((long long)walk.ct * NT + st) / a.H), s.m - 1);
+      const int lim0 = s.kv - s.m + (int)((long long)walk.ct * NT / a.H);
+      float mx[2 * R], sum[2 * R];
+#pragma unroll
+      for (int c = 0; c < 2 * R; ++c) {
+        mx[c] = -INFINITY;
+        sum[c] = 0.f;
+      }
+      meet();  // lim is set; the last piece's reads of red and fac are over
+      for (int i = 0; i < walk.n; ++i, ++it) {
+        const int t0 = (walk.t0 + i) * kLatKT;
+        wait(&s_full[it & 1], (it >> 1) & 1);
+        __syncwarp();
+        fence_after_sync();
+        float x[4 * R];
+        tmem_ld_16x256<R>(la + 4 * NT + (it & 1) * NT, x);
+#pragma unroll
+        for (int e = 0; e < 4 * R; ++e) x[e] *= a.scale_log2;
+        if (t0 + kLatKT - 1 > lim0) {
+#pragma unroll
+          for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (t0 + k0 + 8 * (e >> 1) > lim[8 * j + 2 * (lane & 3) + (e & 1)]) x[4 * j + e] = -INFINITY;
+        }
+        // maximum of each column over the tile
+        float* rd = red + (it % L::RB) * 4 * NT;
+        float tm[2 * R];
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = fmaxf(x[4 * j + e], x[4 * j + 2 + e]);
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            tm[2 * j + e] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          }
+        if (lane < 4) {
+#pragma unroll
+          for (int j = 0; j < R; ++j)
+            *reinterpret_cast<float2*>(rd + sp * NT + 8 * j + 2 * lane) = make_float2(tm[2 * j], tm[2 * j + 1]);
+        }
+        meet();
+        bool grew = false;
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          float2 v = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 u = *reinterpret_cast<const float2*>(rd + q * NT + 8 * j + 2 * (lane & 3));
+            v.x = fmaxf(v.x, u.x);
+            v.y = fmaxf(v.y, u.y);
+          }
+          tm[2 * j] = v.x;
+          tm[2 * j + 1] = v.y;
+          grew |= v.x > mx[2 * j] + 8.f || v.y > mx[2 * j + 1] + 8.f;
+        }
+        // the same data in every warp, so the four agree
+        grew = __any_sync(0xffffffffu, grew);
+        if (grew) {
+#pragma unroll
+          for (int c = 0; c < 2 * R; ++c) {
+            const float m2 = fmaxf(mx[c], tm[c]);
+            const float f = m2 == -INFINITY ? 1.f : ex2(mx[c] - m2);
+            mx[c] = m2;
+            sum[c] *= f;
+            tm[c] = f;
+          }
+          if (i > 0) {
+            if (sp == 0 && lane < 4) {
+#pragma unroll
+              for (int j = 0; j < R; ++j)
+                *reinterpret_cast<float2*>(fac + 8 * j + 2 * lane) = make_float2(tm[2 * j], tm[2 * j + 1]);
+            }
+            meet();
+            wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+            __syncwarp();
+            fence_after_sync();
+#pragma unroll 1
+            for (int c0 = 0; c0 < 4 * NT; c0 += 16) {
+              float v[16];
+              tmem_ld16(la + c0, v);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) v[c] *= fac[(c0 % NT) + c];
+              tmem_st16(la + c0, v);
+            }
+          }
+        }
+        if (L::PB == 1 && i > 0 && !grew) wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1);  // P of the last tile has been read
+        if (L::RB == 1) meet();                                        // everyone has read the maxima
+        // weights: fp32 into the sums, bf16 into the product (the tensor core's operand type; the
+        // rounding errors are independent and average over the row)
+        const uint32_t ph = sb + L::p + (it % L::PB) * NT * 128;
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float m = mx[2 * j + (e & 1)];
+            x[4 * j + e] = ex2(x[4 * j + e] - (m == -INFINITY ? 0.f : m));
+          }
+#pragma unroll
+        for (int c = 0; c < 2 * R; ++c) sum[c] += x[4 * (c >> 1) + (c & 1)] + x[4 * (c >> 1) + 2 + (c & 1)];
+#pragma unroll
+        for (int j = 0; j < R; j += 2) {
+          const int n = 8 * (j + (lane >> 4)) + (lane & 7), chunk = 2 * sp + ((lane >> 3) & 1);
+          stmatrix4_trans(ph + n * 128 + ((chunk ^ (lane & 7)) << 4), pack_bf16(x[4 * j], x[4 * j + 1]),
+                          pack_bf16(x[4 * j + 2], x[4 * j + 3]), pack_bf16(x[4 * j + 4], x[4 * j + 5]),
+                          pack_bf16(x[4 * j + 6], x[4 * j + 7]));
+        }
+        // rows of the tile that hold no token of the sequence: their weights are 0, but whatever the
+        // page holds there (NaN among it) must not meet them
+        const int have = max(s.kv - t0, 0);
+        if (have < kLatKT) {
+          uint8_t* kv = sm + L::stage + (it & 1) * kLatStage;
+          const int units = (kLatKT - have) * 8 * (kLatDim / 64);
+          for (int u = st; u < units; u += 128) {
+            const int c = u / ((kLatKT - have) * 8), r = u % ((kLatKT - have) * 8);
+            *reinterpret_cast<uint4*>(kv + (c * kLatKT + have) * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_async_smem();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[it & 1]);
+      }
+      // ---- end of the piece: sums over the tokens, then O^T out of tensor memory
+#pragma unroll
+      for (int c = 0; c < 2 * R; ++c) {
+        sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 4);
+        sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 8);
+        sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 16);
+      }
+      meet();  // red and fac have been read
+      if (lane < 4) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          *reinterpret_cast<float2*>(red + sp * NT + 8 * j + 2 * lane) = make_float2(sum[2 * j], sum[2 * j + 1]);
+          if (sp == 0) *reinterpret_cast<float2*>(fac + 8 * j + 2 * lane) = make_float2(mx[2 * j], mx[2 * j + 1]);
+        }
+      }
+      meet();
+      const bool whole = walk.t0 == 0 && walk.n == walk.tiles;
+      const int slot = 2 * blockIdx.x + (walk.t0 == 0 ? 1 : 0);
+      const float l = st < NT ? red[st] + red[NT + st] + red[2 * NT + st] + red[3 * NT + st] : 0.f;
+      if (st < ncols) {
+        if (whole)
+          a.lse[col0 + st] = l == 0.f ? -INFINITY : (fac[st] + log2f(l)) * 0.6931471805599453f;
+        else
+          a.ml[slot * kLatMaxNT + st] = make_float2(fac[st], l);
+      }
+      if (!whole && walk.t0 == 0 && st == 0) {
+        const long long rest = walk.tiles - walk.n;
+        a.meta[blockIdx.x] = {col0, ncols, 1 + (int)((rest + per - 1) / per)};
+      }
+      meet();
+      if (st < NT) fac[st] = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      meet();
+      wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+      __syncwarp();
+      fence_after_sync();
+#pragma unroll 1
+      for (int c0 = 0; c0 < 4 * NT; c0 += 16) {
+        float v[16];
+        tmem_ld16(la + c0, v);
+        const int cc = c0 % NT, dim = c0 / NT * 128 + 32 * sp + lane;
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (cc + c < ncols) a.o[(size_t)(col0 + cc + c) * kLatDim + dim] = __float2bfloat16_rn(v[c] * fac[cc + c]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (cc + c < ncols) a.part[((size_t)slot * kLatMaxNT + cc + c) * kLatDim + dim] = v[c];
+        }
+      }
+      fence_before_sync();
+    }
+    if (st == 0 && share == 0) a.meta[blockIdx.x].n = 0;
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (w == 1) tmem_dealloc(tb, NT == 16 ? 128 : NT == 32 ? 256 : 512);
+}
+
+// One CTA per (share, column): joins the pieces of the unit that starts in the share and ends in a
+// later one, in order: o = sum_i e^{m_i - m} O_i / sum_i e^{m_i - m} l_i.  Thread = 4 dimensions.
+__global__ void __launch_bounds__(128) latent_combine_kernel(LatAttnArgs a) {
+  const LatPiece u = a.meta[blockIdx.x];
+  const int c = blockIdx.y;
+  if (u.n == 0 || c >= u.ncols) return;
+  auto slot = [&](int i) { return i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i); };
+  float m = -INFINITY;
+  for (int i = 0; i < u.n; ++i) m = fmaxf(m, a.ml[slot(i) * kLatMaxNT + c].x);
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < u.n; ++i) {
+    const float2 ml = a.ml[slot(i) * kLatMaxNT + c];
+    const float4 x = *reinterpret_cast<const float4*>(a.part + ((size_t)slot(i) * kLatMaxNT + c) * kLatDim + 4 * threadIdx.x);
+    if (ml.x == -INFINITY) continue;
+    const float f = tc::ex2(ml.x - m);
+    l = fmaf(f, ml.y, l);
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  store4(a.o + (size_t)(u.col0 + c) * kLatDim + 4 * threadIdx.x, o);
+  if (threadIdx.x == 0) a.lse[u.col0 + c] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+}  // namespace tpc
