@@ -155,7 +155,7 @@ int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t
   // columns of a tile: the (row, head) pairs that an average sequence has
   const int64_t cols = ((int64_t)r.n_rows * H + r.n_seqs - 1) / r.n_seqs;
   const int NT = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
-  if (!tensor_map(&tkv, lc.data, tpc::kLatWidth, (uint64_t)lc.n_pages * lc.page_size, tpc::kLatWidth, std::min(lc.page_size, tpc::kLatKT)) ||
+  if (!tensor_map(&tkv, lc.data, tpc::kLatWidth, (uint64_t)lc.n_pages * lc.page_size, tpc::kLatWidth, std::min(lc.page_size, tpc::kLatBox)) ||
       !tensor_map(&tq, qa, tpc::kLatWidth, (uint64_t)r.n_rows * H, tpc::kLatWidth, NT))
     return fail(TPC_ERR_CUDA, "latent attention: cuTensorMapEncodeTiled failed");
   char* sc = static_cast<char*>(scratch);

@@ -2,10 +2,12 @@
 //
 // Every head of every new row of a sequence reads the same cached rows [c | kr], so the (row, head)
 // pairs of a sequence are the columns of one product with the cache as its tall operand:
-//   S^T [64 tokens x NT columns] = K [64 x 576] Qa^T,   O^T [512 x NT] += C^T [512 x 64] P^T [64 x NT].
+//   S^T [128 tokens x NT columns] = K [128 x 576] Qa^T,   O^T [512 x NT] += C^T [512 x 128] P^T [128 x NT].
 // The cached tile is the MMA's A operand both times, once K-major and once (its latent part, the same
 // shared memory) MN-major, and is fetched once; the few columns are N, which the tensor core takes
-// in steps of 16 (rows as M would fill 16 of 128 lanes).
+// in steps of 16 (rows as M would fill 16 of 128 lanes).  An MMA with few columns occupies the tensor
+// core for about 70 cycles whatever its M (measured: 80 at M = 64, 69 at M = 128, N = 16), so tiles are
+// 128 tokens: 36 + 32 MMAs, 4,800 cycles, against 6,300 cycles that the tile's 147 KB take from HBM.
 #pragma once
 #include <cuda.h>
 
@@ -15,21 +17,27 @@
 
 namespace tpc {
 
-constexpr int kLatKT = 64;                          // tokens per tile
-constexpr int kLatChunks = kLatWidth / 64;          // 64-column boxes of a cached row (the last one rotary)
+constexpr int kLatKT = 128;                         // tokens per tile
+constexpr int kLatBox = 64;                         // most rows of one TMA box
+constexpr int kLatChunks = kLatWidth / 64;          // 64-column chunks of a cached row (the last one rotary)
+constexpr int kLatItems = 1 + kLatDim / 128;        // slots of a tile: the rotary chunk, then pairs of latent chunks
 constexpr int kLatAttnThreads = 192;                // producer warp, MMA warp, four softmax warps
 constexpr int kLatMaxCtas = 148;
 constexpr int kLatMaxNT = 64;
-constexpr uint32_t kLatStage = kLatChunks * kLatKT * 128;
+constexpr uint32_t kLatChunk = kLatKT * 128, kLatSlot = 2 * kLatChunk;
 
+// A tile goes through a ring of 32 KB slots, so that its slots are refilled one by one: the rotary chunk
+// once the scores have read it, each latent pair once its 128 dimensions are summed.  With four slots
+// (NT = 64) the last pair takes the rotary chunk's place.
 template <int NT>
 struct LatSmem {
-  static constexpr uint32_t PB = NT == 64 ? 1 : 2, RB = PB;  // buffers of P and of the maxima
-  static constexpr uint32_t q = 0, stage = q + kLatChunks * NT * 128, p = stage + 2 * kLatStage, end = p + PB * NT * 128;
-  static constexpr uint32_t red = end, fac = red + RB * 4 * NT * 4, lim = fac + NT * 4, bars = lim + NT * 4;
-  static constexpr uint32_t total = bars + 256 + 1024;  // + slack to align the tiles to 1024 bytes
+  static constexpr uint32_t slots = NT == 16 ? 6 : NT == 32 ? 5 : 4;
+  static constexpr uint32_t q = 0, ring = q + kLatChunks * NT * 128, p = ring + slots * kLatSlot, end = p + 2 * NT * 128;
+  static constexpr uint32_t red = end, fac = red + 2 * 4 * NT * 4, lim = fac + NT * 4, bars = lim + NT * 4;
+  static constexpr uint32_t total = bars + 384 + 1024;  // + slack to align the tiles to 1024 bytes
 };
-static_assert(LatSmem<64>::total <= 232448, "shared memory of one CTA");
+static_assert(LatSmem<64>::total <= 232448 && LatSmem<32>::total <= 232448 && LatSmem<16>::total <= 232448,
+              "shared memory of one CTA");
 
 // scratch: partial sums of the pieces (two per CTA), their (max, sum), and one record per CTA
 struct LatPiece {
@@ -179,19 +187,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // found on the device from kv_len (no host copy, graphs replay with new lengths).  A unit that is cut
 // leaves partial sums for latent_combine_kernel.
 //
-// Warp 0 fetches tiles by TMA (64-column boxes, one per page and column chunk) into two stages, warp 1
-// issues the MMAs, warps 2-5 run the softmax: a warp holds 16 tokens x NT columns of S^T in the
-// 16x256b register layout (all lanes busy although M = 64 fills half the TMEM lanes), maxima over
-// tokens are 3 shuffles and one exchange between the four warps.  Running sums stay per lane until
-// the piece ends.  The maximum is only raised when it grew by more than 8 (base 2): until then the
-// weights are at most 2^8 and the sums of the old maximum stay valid, which saves the pass over O^T.
-// S of tile i + 1 runs on the tensor core while tile i is in the softmax.
+// Warp 0 fetches tiles by TMA (64-column boxes, one per page and column chunk) into the ring and
+// prefetches the following tile into L2, whose latency the ring alone is too small to hide.  Warp 1
+// issues the MMAs: the scores of tile i + 1 as far as its slots have arrived, and the weighted sum of
+// tile i as soon as the weights are there.  Warps 2-5 run the softmax: a warp holds 32 tokens x NT
+// columns of S^T in the 16x256b register layout, maxima over tokens are 3 shuffles and one exchange
+// between the four warps.  Running sums stay per lane until the piece ends.  The maximum is only
+// raised when it grew by more than 8 (base 2): until then the weights are at most 2^8 and the sums of
+// the old maximum stay valid, which saves the pass over O^T.
 template <int NT>
 __global__ void __launch_bounds__(kLatAttnThreads, 1)
     latent_attn_tc(const __grid_constant__ CUtensorMap tma_kv, const __grid_constant__ CUtensorMap tma_q, LatAttnArgs a) {
   using namespace tc;
   using L = LatSmem<NT>;
-  constexpr int R = NT / 8;
+  constexpr int R = NT / 8, U = L::slots;
+  constexpr uint32_t kTmem = NT == 16 ? 128 : NT == 32 ? 256 : 512;
   extern __shared__ __align__(1024) uint8_t lsm_raw[];
   uint8_t* sm = lsm_raw + ((1024u - (smem_u32(lsm_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(sm);
@@ -199,12 +209,12 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
   float* fac = reinterpret_cast<float*>(sm + L::fac);
   int* lim = reinterpret_cast<int*>(sm + L::lim);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
-  uint64_t *full = bars, *empty = bars + 2, *s_full = bars + 4, *p_full = bars + 6, *o_done = bars + 8, *q_full = bars + 10,
-           *q_empty = bars + 11, *done = bars + 12;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 13);
-  int* abort_flag = reinterpret_cast<int*>(bars + 13) + 1;
-  int* where = reinterpret_cast<int*>(bars + 14);               // b, ct, tile of the share's start
-  long long* sums = reinterpret_cast<long long*>(bars + 16);    // per warp
+  uint64_t *full = bars, *empty = bars + 6, *s_full = bars + 12, *p_full = bars + 14, *o_done = bars + 16,
+           *q_full = bars + 18, *q_empty = bars + 19, *done = bars + 20;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 21);
+  int* abort_flag = reinterpret_cast<int*>(bars + 21) + 1;
+  int* where = reinterpret_cast<int*>(bars + 22);             // b, ct, tile of the share's start
+  long long* sums = reinterpret_cast<long long*>(bars + 24);  // per warp
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
 
   // ---- this CTA's share
@@ -223,11 +233,13 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     if (lane >= d) incl += y;
   }
   if (lane == 31) sums[w] = incl;
-  if (w == 1) tmem_alloc(tslot, NT == 16 ? 128 : NT == 32 ? 256 : 512);
+  if (w == 1) tmem_alloc(tslot, kTmem);
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < U; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_done[i], 1);
@@ -268,109 +280,153 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
   auto aborted = [&] { return *((volatile int*)abort_flag) != 0; };
   // Every wait is bounded.  After the first that runs out no role waits, copies or multiplies any
   // more, but all walk on to the end of their loops, so the barriers between the softmax warps match.
+  auto give_up = [&] {
+    set_status(a.status, 8);
+    atomicExch(abort_flag, 1);
+  };
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (aborted()) return false;
     if (mbar_wait(bar, parity, 2000000000ull)) return true;
-    set_status(a.status, 8);
-    atomicExch(abort_flag, 1);
+    give_up();
     return false;
   };
 
   if (w == 0) {  // ---- producer
-    const int ps = a.cache.page_size, box = min(ps, kLatKT);
-    int it = 0, piece = 0;
-    for (; walk.left > 0; walk.next(), ++piece) {
-      const LatSeq s = walk.s;
-      const int32_t* table = a.cache.table + (size_t)walk.b * a.cache.max_pages;
-      bool ok = piece == 0 || wait(q_empty, (piece - 1) & 1);
-      if (lane == 0 && ok) {
-        mbar_arrive_expect_tx(q_full, kLatChunks * NT * 128);
-        for (int c = 0; c < kLatChunks; ++c)
-          tma_load_2d(sm + L::q + c * NT * 128, &tma_q, 64 * c, s.row0 * a.H + walk.ct * NT, q_full);
-      }
-      for (int i = 0; i < walk.n; ++i, ++it) {
-        const int t0 = (walk.t0 + i) * kLatKT, st = it & 1;
-        const int segs = (min(max(s.kv - t0, 0), kLatKT) + box - 1) / box;
-        // this lane's boxes: (segment, chunk) pairs lane and lane + 32; their pages are read before the wait
-        int row[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = lane + 32 * e, tok = t0 + j / kLatChunks * box;
-          row[e] = 0;
-          if (j < segs * kLatChunks) {
-            int page = table[tok / ps];
-            if (page < 0 || page >= a.cache.n_pages) {
-              set_status(a.status, kStatusCheck);
-              page = 0;
-            }
-            row[e] = page * ps + tok % ps;
-          }
+    const int ps = a.cache.page_size, box = min(ps, kLatBox);
+    struct Tile {
+      bool valid, first;
+      int segs, row, q_row;  // row: first cache row of segment `lane`
+    };
+    int ahead = 0;           // tile of the walk's piece that fetch() returns next
+    auto fetch = [&]() -> Tile {
+      Tile t{walk.left > 0, ahead == 0, 0, 0, 0};
+      if (!t.valid) return t;
+      const int t0 = (walk.t0 + ahead) * kLatKT;
+      t.segs = (min(max(walk.s.kv - t0, 0), kLatKT) + box - 1) / box;
+      t.q_row = walk.s.row0 * a.H + walk.ct * NT;
+      if (lane < t.segs) {
+        const int tok = t0 + lane * box;
+        int page = a.cache.table[(size_t)walk.b * a.cache.max_pages + tok / ps];
+        if (page < 0 || page >= a.cache.n_pages) {
+          set_status(a.status, kStatusCheck);
+          page = 0;
         }
-        ok = it < 2 || wait(&empty[st], ((it >> 1) - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) continue;
+        t.row = page * ps + tok % ps;
+      }
+      if (++ahead == walk.n) {
+        ahead = 0;
+        walk.next();
+      }
+      return t;
+    };
+    int item = 0, piece = -1;
+    Tile cur = fetch();
+    while (cur.valid) {
+      const Tile nxt = fetch();
+      if (lane < nxt.segs) bulk_prefetch_l2(a.cache.data + (size_t)nxt.row * kLatWidth, box * kLatWidth * 2);
+      if (cur.first) {
+        ++piece;
+        if ((piece == 0 || wait(q_empty, (piece - 1) & 1)) && lane == 0) {
+          mbar_arrive_expect_tx(q_full, kLatChunks * NT * 128);
+          for (int c = 0; c < kLatChunks; ++c) tma_load_2d(sm + L::q + c * NT * 128, &tma_q, 64 * c, cur.q_row, q_full);
+        }
+      }
+      for (int e = 0; e < kLatItems; ++e, ++item) {
+        const int st = item % U, nc = e == 0 ? 1 : 2;  // chunks of the item: 8, then 0 1, 2 3, 4 5, 6 7
+        const bool ok = item < U || wait(&empty[st], (item / U - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) continue;
         if (lane == 0) {
-          if (segs)
-            mbar_arrive_expect_tx(&full[st], segs * kLatChunks * box * 128);
+          if (cur.segs)
+            mbar_arrive_expect_tx(&full[st], cur.segs * nc * box * 128);
           else
             mbar_arrive(&full[st]);
         }
         __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = lane + 32 * e, seg = j / kLatChunks, c = j % kLatChunks;
-          if (j < segs * kLatChunks)
-            tma_load_2d(sm + L::stage + st * kLatStage + (c * kLatKT + seg * box) * 128, &tma_kv, 64 * c, row[e], &full[st]);
-        }
+        const int seg = lane / nc, c = lane % nc;
+        const int row = __shfl_sync(0xffffffffu, cur.row, seg);
+        if (seg < cur.segs)
+          tma_load_2d(sm + L::ring + st * kLatSlot + c * kLatChunk + seg * box * 128, &tma_kv,
+                      64 * (e == 0 ? kLatChunks - 1 : 2 * (e - 1) + c), row, &full[st]);
       }
+      cur = nxt;
     }
     if (aborted() && lane == 0) {  // copies in flight land before the CTA ends
-      for (int i = max(0, it - 2); i < it; ++i) mbar_wait(&full[i & 1], (i >> 1) & 1, 100000000ull);
-      mbar_wait(q_full, (piece - 1) & 1, 100000000ull);
+      for (int i = max(0, item - U); i < item; ++i) mbar_wait(&full[i % U], (i / U) & 1, 100000000ull);
+      if (piece >= 0) mbar_wait(q_full, piece & 1, 100000000ull);
     }
   } else if (w == 1) {  // ---- MMA
     if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16(64, NT, false, false), id_o = idesc_bf16(128, NT, true, false);
-      int it = 0, piece = 0;
-      auto weighted_sum = [&](int i, bool first) {  // O^T (+)= C^T P^T of tile i
-        if (!wait(&p_full[i & 1], (i >> 1) & 1)) return;
+      constexpr uint32_t id_s = idesc_bf16(128, NT, false, false), id_o = idesc_bf16(128, NT, true, false);
+      int it = 0, piece = 0, pend = -1;  // pend: tile whose weighted sum is not issued yet
+      bool pend_first = false;
+      auto weighted_sum = [&] {  // O^T (+)= C^T P^T of the pending tile
         fence_after_sync();
-        const uint32_t kv = sb + L::stage + (i & 1) * kLatStage, p = sb + L::p + (i % L::PB) * NT * 128;
-#pragma unroll
-        for (int mb = 0; mb < 4; ++mb)
+        const uint32_t p = sb + L::p;
+#pragma unroll 1
+        for (int mb = 0; mb < 4; ++mb) {
+          const int st = (pend * kLatItems + 1 + mb) % U;
+          const uint32_t kv = sb + L::ring + st * kLatSlot;
 #pragma unroll
           for (int ks = 0; ks < kLatKT / 16; ++ks)
-            mma_bf16(tb + mb * NT, sw_desc_mn(kv + 2 * mb * kLatKT * 128, kLatKT, ks), sw_desc_k(p, NT, ks), id_o,
-                     first && ks == 0 ? 0u : 1u);
-        commit(&o_done[i & 1]);
-        commit(&empty[i & 1]);
+            mma_bf16(tb + mb * NT, sw_desc_mn(kv, kLatKT, ks), sw_desc_k(p, NT, ks), id_o, pend_first && ks == 0 ? 0u : 1u);
+          if (mb == 3) commit(&o_done[pend & 1]);
+          commit(&empty[st]);
+        }
+        pend = -1;
+      };
+      // waits for the barrier and issues the pending sum meanwhile, on which the barrier may depend
+      auto wait_or_sum = [&](uint64_t* bar, uint32_t parity) -> bool {
+        uint64_t t0 = 0;
+        while (!aborted()) {
+          if (pend >= 0 && mbar_try_wait(&p_full[pend & 1], (pend >> 1) & 1)) weighted_sum();
+          if (mbar_try_wait(bar, parity)) return true;
+          const uint64_t t = globaltimer();
+          if (t0 == 0) t0 = t;
+          if (t - t0 > 2000000000ull) give_up();
+        }
+        return false;
       };
       for (; walk.left > 0; walk.next(), ++piece) {
-        wait(q_full, piece & 1);
+        wait_or_sum(q_full, piece & 1);
         for (int i = 0; i < walk.n; ++i, ++it) {
-          if (wait(&full[it & 1], (it >> 1) & 1)) {
+          const uint32_t acc = tb + 4 * NT + (it & 1) * NT;
+          for (int e = 0; e < kLatItems; ++e) {
+            const int item = it * kLatItems + e, st = item % U;
+            if (!wait_or_sum(&full[st], (item / U) & 1)) continue;
             fence_after_sync();
-            const uint32_t kv = sb + L::stage + (it & 1) * kLatStage;
-#pragma unroll 4
-            for (int ks = 0; ks < kLatWidth / 16; ++ks)
-              mma_bf16(tb + 4 * NT + (it & 1) * NT, sw_desc_k(kv, kLatKT, ks), sw_desc_k(sb + L::q, NT, ks), id_s, ks ? 1u : 0u);
+            const uint32_t kv = sb + L::ring + st * kLatSlot;
+            if (e == 0) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_bf16(acc, sw_desc_k(kv, kLatKT, ks), sw_desc_k(sb + L::q, NT, 4 * (kLatChunks - 1) + ks), id_s, ks ? 1u : 0u);
+              commit(&empty[st]);
+            } else {
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                mma_bf16(acc, sw_desc_k(kv, kLatKT, ks), sw_desc_k(sb + L::q, NT, 8 * (e - 1) + ks), id_s, 1u);
+            }
+          }
+          if (!aborted()) {
             commit(&s_full[it & 1]);
             if (i == walk.n - 1) commit(q_empty);
           }
-          if (i > 0) weighted_sum(it - 1, i == 1);
+          // the previous tile's sum before this one becomes the pending one
+          if (pend >= 0 && wait(&p_full[pend & 1], (pend >> 1) & 1)) weighted_sum();
+          pend = it;
+          pend_first = i == 0;
         }
-        weighted_sum(it - 1, walk.n == 1);
       }
+      if (pend >= 0 && wait(&p_full[pend & 1], (pend >> 1) & 1)) weighted_sum();
       commit(done);
       if (!mbar_wait(done, 0, 2000000000ull)) set_status(a.status, 8);
     }
-  } else {  // ---- softmax warps: sub-partition sp holds tokens 16 sp .. 16 sp + 15 of a tile, and
+  } else {  // ---- softmax warps: sub-partition sp holds tokens 32 sp .. 32 sp + 31 of a tile, and
             //      latent dimensions 32 sp .. 32 sp + 31 of each 128-row block of O^T
-    const int sp = w & 3, k0 = 16 * sp + (lane >> 2), st = tid - 64;
+    const int sp = w & 3, k0 = 32 * sp + (lane >> 2), st = tid - 64;
     const uint32_t la = tb + ((uint32_t)(32 * sp) << 16);
     auto meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
     int it = 0;
-    if (st == 0 && share > 0) a.meta[blockIdx.x].n = 0;
+    if (st == 0) a.meta[blockIdx.x].n = 0;
     for (; walk.left > 0; walk.next()) {
       const LatSeq s = walk.s;
       const long long col0 = (long long)s.row0 * a.H + (long long)walk.ct * NT;
@@ -390,29 +446,26 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
         wait(&s_full[it & 1], (it >> 1) & 1);
         __syncwarp();
         fence_after_sync();
-        float x[4 * R];
-        tmem_ld_16x256<R>(la + 4 * NT + (it & 1) * NT, x);
-#pragma unroll
-        for (int e = 0; e < 4 * R; ++e) x[e] *= a.scale_log2;
-        if (t0 + kLatKT - 1 > lim0) {
-#pragma unroll
-          for (int j = 0; j < R; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (t0 + k0 + 8 * (e >> 1) > lim[8 * j + 2 * (lane & 3) + (e & 1)]) x[4 * j + e] = -INFINITY;
-        }
-        // maximum of each column over the tile
-        float* rd = red + (it % L::RB) * 4 * NT;
+        float x[2][4 * R];  // [16-token half][...]
+        tmem_ld_16x256<R>(la + 4 * NT + (it & 1) * NT, x[0]);
+        tmem_ld_16x256<R>(la + (16u << 16) + 4 * NT + (it & 1) * NT, x[1]);
+        const bool mask = t0 + kLatKT - 1 > lim0;
         float tm[2 * R];
 #pragma unroll
-        for (int j = 0; j < R; ++j)
+        for (int c = 0; c < 2 * R; ++c) {  // maximum of each column over the tile
+          float v = -INFINITY;
+          const int last = mask ? lim[8 * (c >> 1) + 2 * (lane & 3) + (c & 1)] : 0;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v = fmaxf(x[4 * j + e], x[4 * j + 2 + e]);
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-            tm[2 * j + e] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          for (int g = 0; g < 4; ++g) {
+            float& y = x[g >> 1][4 * (c >> 1) + 2 * (g & 1) + (c & 1)];
+            y = mask && t0 + k0 + 8 * g > last ? -INFINITY : y * a.scale_log2;
+            v = fmaxf(v, y);
           }
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          tm[c] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        }
+        float* rd = red + (it & 1) * 4 * NT;
         if (lane < 4) {
 #pragma unroll
           for (int j = 0; j < R; ++j)
@@ -444,16 +497,18 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
             sum[c] *= f;
             tm[c] = f;
           }
-          if (i > 0) {
+        }
+        if (i > 0) {  // the last tile's weights have been read, and its sum is complete
+          wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+          __syncwarp();
+          fence_after_sync();
+          if (grew) {
             if (sp == 0 && lane < 4) {
 #pragma unroll
               for (int j = 0; j < R; ++j)
                 *reinterpret_cast<float2*>(fac + 8 * j + 2 * lane) = make_float2(tm[2 * j], tm[2 * j + 1]);
             }
             meet();
-            wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
-            __syncwarp();
-            fence_after_sync();
 #pragma unroll 1
             for (int c0 = 0; c0 < 4 * NT; c0 += 16) {
               float v[16];
@@ -464,36 +519,36 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
             }
           }
         }
-        if (L::PB == 1 && i > 0 && !grew) wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1);  // P of the last tile has been read
-        if (L::RB == 1) meet();                                        // everyone has read the maxima
         // weights: fp32 into the sums, bf16 into the product (the tensor core's operand type; the
         // rounding errors are independent and average over the row)
-        const uint32_t ph = sb + L::p + (it % L::PB) * NT * 128;
 #pragma unroll
-        for (int j = 0; j < R; ++j)
+        for (int c = 0; c < 2 * R; ++c) {
+          const float m = mx[c] == -INFINITY ? 0.f : mx[c];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float m = mx[2 * j + (e & 1)];
-            x[4 * j + e] = ex2(x[4 * j + e] - (m == -INFINITY ? 0.f : m));
+          for (int g = 0; g < 4; ++g) {
+            float& y = x[g >> 1][4 * (c >> 1) + 2 * (g & 1) + (c & 1)];
+            y = ex2(y - m);
+            sum[c] += y;
           }
-#pragma unroll
-        for (int c = 0; c < 2 * R; ++c) sum[c] += x[4 * (c >> 1) + (c & 1)] + x[4 * (c >> 1) + 2 + (c & 1)];
-#pragma unroll
-        for (int j = 0; j < R; j += 2) {
-          const int n = 8 * (j + (lane >> 4)) + (lane & 7), chunk = 2 * sp + ((lane >> 3) & 1);
-          stmatrix4_trans(ph + n * 128 + ((chunk ^ (lane & 7)) << 4), pack_bf16(x[4 * j], x[4 * j + 1]),
-                          pack_bf16(x[4 * j + 2], x[4 * j + 3]), pack_bf16(x[4 * j + 4], x[4 * j + 5]),
-                          pack_bf16(x[4 * j + 6], x[4 * j + 7]));
         }
+        const uint32_t ph = sb + L::p + (sp >> 1) * NT * 128;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int j = 0; j < R; j += 2) {
+            const int n = 8 * (j + (lane >> 4)) + (lane & 7), unit = 4 * (sp & 1) + 2 * g + ((lane >> 3) & 1);
+            stmatrix4_trans(ph + n * 128 + ((unit ^ (lane & 7)) << 4), pack_bf16(x[g][4 * j], x[g][4 * j + 1]),
+                            pack_bf16(x[g][4 * j + 2], x[g][4 * j + 3]), pack_bf16(x[g][4 * j + 4], x[g][4 * j + 5]),
+                            pack_bf16(x[g][4 * j + 6], x[g][4 * j + 7]));
+          }
         // rows of the tile that hold no token of the sequence: their weights are 0, but whatever the
         // page holds there (NaN among it) must not meet them
         const int have = max(s.kv - t0, 0);
         if (have < kLatKT) {
-          uint8_t* kv = sm + L::stage + (it & 1) * kLatStage;
-          const int units = (kLatKT - have) * 8 * (kLatDim / 64);
-          for (int u = st; u < units; u += 128) {
-            const int c = u / ((kLatKT - have) * 8), r = u % ((kLatKT - have) * 8);
-            *reinterpret_cast<uint4*>(kv + (c * kLatKT + have) * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+          const int per_chunk = (kLatKT - have) * 8;
+          for (int c = 0; c < kLatDim / 64; ++c) {
+            uint8_t* row = sm + L::ring + ((it * kLatItems + 1 + (c >> 1)) % U) * kLatSlot + (c & 1) * kLatChunk + have * 128;
+            for (int u = st; u < per_chunk; u += 128) *reinterpret_cast<uint4*>(row + u * 16) = make_uint4(0, 0, 0, 0);
           }
         }
         fence_async_smem();
@@ -553,11 +608,10 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       }
       fence_before_sync();
     }
-    if (st == 0 && share == 0) a.meta[blockIdx.x].n = 0;
   }
   fence_before_sync();
   __syncthreads();
-  if (w == 1) tmem_dealloc(tb, NT == 16 ? 128 : NT == 32 ? 256 : 512);
+  if (w == 1) tmem_dealloc(tb, kTmem);
 }
 
 // One CTA per (share, column): joins the pieces of the unit that starts in the share and ends in a
