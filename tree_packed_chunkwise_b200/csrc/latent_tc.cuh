@@ -355,71 +355,84 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       if (piece >= 0) mbar_wait(q_full, piece & 1, 100000000ull);
     }
   } else if (w == 1) {  // ---- MMA
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16(128, NT, false, false), id_o = idesc_bf16(128, NT, true, false);
-      int it = 0, piece = 0, pend = -1;  // pend: tile whose weighted sum is not issued yet
-      bool pend_first = false;
-      auto weighted_sum = [&] {  // O^T (+)= C^T P^T of the pending tile
-        fence_after_sync();
-        const uint32_t p = sb + L::p;
-#pragma unroll 1
-        for (int mb = 0; mb < 4; ++mb) {
-          const int st = (pend * kLatItems + 1 + mb) % U;
-          const uint32_t kv = sb + L::ring + st * kLatSlot;
+    // The whole warp walks the loops and one elected lane issues, so that descriptors stay in uniform
+    // registers.
+    const uint32_t lead = elect_one();
+    constexpr uint32_t id_s = idesc_bf16(128, NT, false, false), id_o = idesc_bf16(128, NT, true, false);
+    // descriptors of slot 0 and of step 0; the low word holds address / 16
+    const uint64_t d_kv_k = sw_desc_k(sb + L::ring, kLatKT, 0), d_kv_mn = sw_desc_mn(sb + L::ring, kLatKT, 0);
+    const uint64_t d_q = sw_desc_k(sb + L::q, NT, 0), d_p = sw_desc_k(sb + L::p, NT, 0);
+    auto k_step = [](int rows, int ks) { return (uint64_t)(((ks >> 2) * rows * 128 + (ks & 3) * 32) >> 4); };
+    int it = 0, piece = 0, slot = 0, pend = -1;  // slot: of the next item; pend: tile whose weighted sum is not issued yet
+    int pend_slot = 0;                           // slot of its first latent pair
+    uint32_t pend_acc = 0;
+    auto weighted_sum = [&] {  // O^T (+)= C^T P^T of the pending tile
+      fence_after_sync();
+      int st = pend_slot;
 #pragma unroll
-          for (int ks = 0; ks < kLatKT / 16; ++ks)
-            mma_bf16(tb + mb * NT, sw_desc_mn(kv, kLatKT, ks), sw_desc_k(p, NT, ks), id_o, pend_first && ks == 0 ? 0u : 1u);
-          if (mb == 3) commit(&o_done[pend & 1]);
-          commit(&empty[st]);
-        }
-        pend = -1;
-      };
-      // waits for the barrier and issues the pending sum meanwhile, on which the barrier may depend
-      auto wait_or_sum = [&](uint64_t* bar, uint32_t parity) -> bool {
-        uint64_t t0 = 0;
-        while (!aborted()) {
-          if (pend >= 0 && mbar_try_wait(&p_full[pend & 1], (pend >> 1) & 1)) weighted_sum();
-          if (mbar_try_wait(bar, parity)) return true;
-          const uint64_t t = globaltimer();
-          if (t0 == 0) t0 = t;
-          if (t - t0 > 2000000000ull) give_up();
-        }
-        return false;
-      };
-      for (; walk.left > 0; walk.next(), ++piece) {
-        wait_or_sum(q_full, piece & 1);
-        for (int i = 0; i < walk.n; ++i, ++it) {
-          const uint32_t acc = tb + 4 * NT + (it & 1) * NT;
-          for (int e = 0; e < kLatItems; ++e) {
-            const int item = it * kLatItems + e, st = item % U;
-            if (!wait_or_sum(&full[st], (item / U) & 1)) continue;
-            fence_after_sync();
-            const uint32_t kv = sb + L::ring + st * kLatSlot;
-            if (e == 0) {
+      for (int mb = 0; mb < 4; ++mb) {
+        const uint64_t d = d_kv_mn + (uint64_t)(st * (kLatSlot >> 4));
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                mma_bf16(acc, sw_desc_k(kv, kLatKT, ks), sw_desc_k(sb + L::q, NT, 4 * (kLatChunks - 1) + ks), id_s, ks ? 1u : 0u);
-              commit(&empty[st]);
-            } else {
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                mma_bf16(acc, sw_desc_k(kv, kLatKT, ks), sw_desc_k(sb + L::q, NT, 8 * (e - 1) + ks), id_s, 1u);
-            }
-          }
-          if (!aborted()) {
-            commit(&s_full[it & 1]);
-            if (i == walk.n - 1) commit(q_empty);
-          }
-          // the previous tile's sum before this one becomes the pending one
-          if (pend >= 0 && wait(&p_full[pend & 1], (pend >> 1) & 1)) weighted_sum();
-          pend = it;
-          pend_first = i == 0;
-        }
+        for (int ks = 0; ks < kLatKT / 16; ++ks)
+          mma_bf16_if(lead, tb + mb * NT, d + (uint64_t)(ks * (2048 >> 4)), d_p + k_step(NT, ks), id_o, ks ? 1u : pend_acc);
+        if (mb == 3) commit_if(lead, &o_done[pend & 1]);
+        commit_if(lead, &empty[st]);
+        st = st + 1 == U ? 0 : st + 1;
       }
-      if (pend >= 0 && wait(&p_full[pend & 1], (pend >> 1) & 1)) weighted_sum();
-      commit(done);
-      if (!mbar_wait(done, 0, 2000000000ull)) set_status(a.status, 8);
+      pend = -1;
+    };
+    // waits for the barrier and issues the pending sum meanwhile, on which the barrier may depend
+    auto wait_or_sum = [&](uint64_t* bar, uint32_t parity) -> bool {
+      uint64_t t0 = 0;
+      while (!__any_sync(0xffffffffu, aborted())) {
+        if (pend >= 0 && __all_sync(0xffffffffu, mbar_try_wait(&p_full[pend & 1], (pend >> 1) & 1))) weighted_sum();
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        const uint64_t t = globaltimer();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > 2000000000ull) give_up();
+      }
+      return false;
+    };
+    auto sum_now = [&] {
+      if (pend >= 0 && __all_sync(0xffffffffu, wait(&p_full[pend & 1], (pend >> 1) & 1))) weighted_sum();
+    };
+    for (; walk.left > 0; walk.next(), ++piece) {
+      wait_or_sum(q_full, piece & 1);
+      const int n = __shfl_sync(0xffffffffu, walk.n, 0);
+      for (int i = 0; i < n; ++i, ++it) {
+        const uint32_t acc = tb + 4 * NT + (it & 1) * NT;
+#pragma unroll
+        for (int e = 0; e < kLatItems; ++e) {
+          const int st = slot;
+          slot = slot + 1 == U ? 0 : slot + 1;
+          if (!wait_or_sum(&full[st], ((it * kLatItems + e) / U) & 1)) continue;
+          fence_after_sync();
+          const uint64_t d = d_kv_k + (uint64_t)(st * (kLatSlot >> 4));
+          if (e == 0) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_if(lead, acc, d + k_step(kLatKT, ks), d_q + k_step(NT, 4 * (kLatChunks - 1) + ks), id_s, ks ? 1u : 0u);
+            commit_if(lead, &empty[st]);
+          } else {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              mma_bf16_if(lead, acc, d + k_step(kLatKT, ks), d_q + k_step(NT, 8 * (e - 1) + ks), id_s, 1u);
+          }
+        }
+        if (!__any_sync(0xffffffffu, aborted())) {
+          commit_if(lead, &s_full[it & 1]);
+          if (i == n - 1) commit_if(lead, q_empty);
+        }
+        sum_now();  // the previous tile's sum before this one becomes the pending one
+        pend = it;
+        pend_acc = i > 0 ? 1u : 0u;
+        pend_slot = slot >= 4 ? slot - 4 : slot - 4 + U;
+      }
     }
+    sum_now();
+    commit_if(lead, done);
+    if (!mbar_wait(done, 0, 2000000000ull)) set_status(a.status, 8);
+    __syncwarp();
   } else {  // ---- softmax warps: sub-partition sp holds tokens 32 sp .. 32 sp + 31 of a tile, and
             //      latent dimensions 32 sp .. 32 sp + 31 of each 128-row block of O^T
     const int sp = w & 3, k0 = 32 * sp + (lane >> 2), st = tid - 64;
