@@ -167,7 +167,16 @@ int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t
     constexpr size_t smem = tpc::LatSmem<N>::total;
     TPC_CUDA(set_smem(tpc::latent_attn_tc<N>, smem));
     TPC_LAUNCH("latent_attn_tc", st, (tpc::latent_attn_tc<N><<<grid, tpc::kLatAttnThreads, smem, st>>>(tkv, tq, a)));
-    TPC_LAUNCH("latent_combine", st, (tpc::latent_combine_kernel<<<dim3(grid, N), 128, 0, st>>>(a)));
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * grid);
+    cfg.blockDim = dim3(tpc::kLatCombThreads);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    TPC_LAUNCH("latent_combine", st, TPC_CUDA(cudaLaunchKernelEx(&cfg, tpc::latent_combine_kernel, a, grid)));
     return TPC_OK;
   };
   if (NT == 16) return go(std::integral_constant<int, 16>{});

@@ -187,9 +187,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // found on the device from kv_len (no host copy, graphs replay with new lengths).  A unit that is cut
 // leaves partial sums for latent_combine_kernel.
 //
-// Warp 0 fetches tiles by TMA (64-column boxes, one per page and column chunk) into the ring and
-// prefetches the following tile into L2, whose latency the ring alone is too small to hide.  Warp 1
-// issues the MMAs: the scores of tile i + 1 as far as its slots have arrived, and the weighted sum of
+// Warp 0 fetches tiles by TMA (64-column boxes, one per page and column chunk) into the ring (a prefetch
+// of the next tile into L2 beside it measured 2 % slower).  Warp 1 issues the MMAs: the scores of tile i + 1 as far as its slots have arrived, and the weighted sum of
 // tile i as soon as the weights are there.  Warps 2-5 run the softmax: a warp holds 32 tokens x NT
 // columns of S^T in the 16x256b register layout, maxima over tokens are 3 shuffles and one exchange
 // between the four warps.  Running sums stay per lane until the piece ends.  The maximum is only
@@ -216,6 +215,10 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
   int* where = reinterpret_cast<int*>(bars + 22);             // b, ct, tile of the share's start
   long long* sums = reinterpret_cast<long long*>(bars + 24);  // per warp
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    prefetch_tensor_map(&tma_kv);
+    prefetch_tensor_map(&tma_q);
+  }
 
   // ---- this CTA's share
   const int lo = (int)((long long)a.rows.n_seqs * tid / kLatAttnThreads);
@@ -256,7 +259,8 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     if (i < w) incl += sums[i];
     total += sums[i];
   }
-  const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)a.min_tiles);
+  long long per = total <= INT32_MAX ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
+  per = max(per, (long long)a.min_tiles);
   const long long start = per * blockIdx.x, share = max(0ll, min(per, total - start));
   if (share > 0 && start >= incl - mine && start < incl) {
     long long at = start - (incl - mine);
@@ -275,6 +279,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     }
   }
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // latent_combine_kernel waits for this grid's end itself
   const uint32_t tb = *tslot;
   LatWalk<NT> walk(a, where[0], where[1], where[2], share);
   auto aborted = [&] { return *((volatile int*)abort_flag) != 0; };
@@ -295,23 +300,19 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     const int ps = a.cache.page_size, box = min(ps, kLatBox);
     struct Tile {
       bool valid, first;
-      int segs, row, q_row;  // row: first cache row of segment `lane`
+      int segs, page, off, q_row;  // page of segment `lane` as the table holds it, first row inside it
     };
-    int ahead = 0;           // tile of the walk's piece that fetch() returns next
-    auto fetch = [&]() -> Tile {
-      Tile t{walk.left > 0, ahead == 0, 0, 0, 0};
+    int ahead = 0;                 // tile of the walk's piece that fetch() returns next
+    auto fetch = [&]() -> Tile {   // only loads the page number: it is looked at a tile later
+      Tile t{walk.left > 0, ahead == 0, 0, 0, 0, 0};
       if (!t.valid) return t;
       const int t0 = (walk.t0 + ahead) * kLatKT;
       t.segs = (min(max(walk.s.kv - t0, 0), kLatKT) + box - 1) / box;
       t.q_row = walk.s.row0 * a.H + walk.ct * NT;
       if (lane < t.segs) {
         const int tok = t0 + lane * box;
-        int page = a.cache.table[(size_t)walk.b * a.cache.max_pages + tok / ps];
-        if (page < 0 || page >= a.cache.n_pages) {
-          set_status(a.status, kStatusCheck);
-          page = 0;
-        }
-        t.row = page * ps + tok % ps;
+        t.page = a.cache.table[(size_t)walk.b * a.cache.max_pages + tok / ps];
+        t.off = tok % ps;
       }
       if (++ahead == walk.n) {
         ahead = 0;
@@ -320,10 +321,13 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       return t;
     };
     int item = 0, piece = -1;
-    Tile cur = fetch();
+    Tile cur = fetch(), nxt = cur;
     while (cur.valid) {
-      const Tile nxt = fetch();
-      if (lane < nxt.segs) bulk_prefetch_l2(a.cache.data + (size_t)nxt.row * kLatWidth, box * kLatWidth * 2);
+      if (cur.page < 0 || cur.page >= a.cache.n_pages) {
+        set_status(a.status, kStatusCheck);
+        cur.page = 0;
+      }
+      const int my_row = cur.page * ps + cur.off;
       if (cur.first) {
         ++piece;
         if ((piece == 0 || wait(q_empty, (piece - 1) & 1)) && lane == 0) {
@@ -333,6 +337,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       }
       for (int e = 0; e < kLatItems; ++e, ++item) {
         const int st = item % U, nc = e == 0 ? 1 : 2;  // chunks of the item: 8, then 0 1, 2 3, 4 5, 6 7
+        if (e == 1) nxt = fetch();
         const bool ok = item < U || wait(&empty[st], (item / U - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) continue;
         if (lane == 0) {
@@ -343,7 +348,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
         }
         __syncwarp();
         const int seg = lane / nc, c = lane % nc;
-        const int row = __shfl_sync(0xffffffffu, cur.row, seg);
+        const int row = __shfl_sync(0xffffffffu, my_row, seg);
         if (seg < cur.segs)
           tma_load_2d(sm + L::ring + st * kLatSlot + c * kLatChunk + seg * box * 128, &tma_kv,
                       64 * (e == 0 ? kLatChunks - 1 : 2 * (e - 1) + c), row, &full[st]);
@@ -627,33 +632,119 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
   if (w == 1) tmem_dealloc(tb, kTmem);
 }
 
-// One CTA per (share, column): joins the pieces of the unit that starts in the share and ends in a
-// later one, in order: o = sum_i e^{m_i - m} O_i / sum_i e^{m_i - m} l_i.  Thread = 4 dimensions.
-__global__ void __launch_bounds__(128) latent_combine_kernel(LatAttnArgs a) {
-  const LatPiece u = a.meta[blockIdx.x];
-  const int c = blockIdx.y;
-  if (u.n == 0 || c >= u.ncols) return;
-  auto slot = [&](int i) { return i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i); };
-  float m = -INFINITY;
-  for (int i = 0; i < u.n; ++i) m = fmaxf(m, a.ml[slot(i) * kLatMaxNT + c].x);
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < u.n; ++i) {
-    const float2 ml = a.ml[slot(i) * kLatMaxNT + c];
-    const float4 x = *reinterpret_cast<const float4*>(a.part + ((size_t)slot(i) * kLatMaxNT + c) * kLatDim + 4 * threadIdx.x);
-    if (ml.x == -INFINITY) continue;
-    const float f = tc::ex2(ml.x - m);
-    l = fmaf(f, ml.y, l);
-    acc.x = fmaf(f, x.x, acc.x);
-    acc.y = fmaf(f, x.y, acc.y);
-    acc.z = fmaf(f, x.z, acc.z);
-    acc.w = fmaf(f, x.w, acc.w);
+// Joins the pieces of every unit that starts in one share and ends in a later one:
+//   o = sum_i e^{m_i - m} O_i / sum_i e^{m_i - m} l_i,
+// in an order that depends on the number of pieces alone.  Launched while the attention kernel still
+// runs (it waits for that grid's end).  The CTAs share a list of work items: a ragged batch leaves a
+// unit per share with two or three pieces (item: four columns, a group of 128 threads each, thread = 4
+// dimensions), one long context a single unit with a piece per share (item: 128 dimensions of one
+// column, 16 warps with every 16th piece each, so that the loads overlap).  One CTA per column
+// instead: 64 x 16384 tokens 11.5 us and one context of 65536 19.7 us.
+constexpr int kLatCombThreads = 512, kLatCombFew = 8;
+__global__ void __launch_bounds__(kLatCombThreads) latent_combine_kernel(LatAttnArgs a, int shares) {
+  __shared__ LatPiece unit[kLatMaxCtas];
+  __shared__ int ends[kLatMaxCtas];  // items of units 0 .. i
+  __shared__ int part_sum[kLatCombThreads / 32];
+  __shared__ float f[kLatMaxCtas];
+  __shared__ float4 acc_s[kLatCombThreads];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int cnt = 0;
+  if (tid < shares) {
+    unit[tid] = a.meta[tid];
+    cnt = unit[tid].n == 0 ? 0 : unit[tid].n <= kLatCombFew ? (unit[tid].ncols + 3) / 4 : 4 * unit[tid].ncols;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-  store4(a.o + (size_t)(u.col0 + c) * kLatDim + 4 * threadIdx.x, o);
-  if (threadIdx.x == 0) a.lse[u.col0 + c] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, cnt, d);
+    if (lane >= d) cnt += y;
+  }
+  if (lane == 31) part_sum[w] = cnt;
+  __syncthreads();
+  for (int i = 0; i < w; ++i) cnt += part_sum[i];
+  if (tid < shares) ends[tid] = cnt;
+  __syncthreads();
+  const int items = ends[shares - 1];
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    int s = 0;  // the unit: as many as end at or before the item
+    for (int i = lane; i < kLatMaxCtas; i += 32) s += i < shares && ends[i] <= item;
+    s = __reduce_add_sync(0xffffffffu, s);
+    const LatPiece u = unit[s];
+    const int k = item - (s ? ends[s - 1] : 0);
+    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * s + 1 : 2 * (s + i)) * kLatMaxNT; };
+    if (u.n <= kLatCombFew) {
+      const int c = 4 * k + (tid >> 7), d = 4 * (tid & 127);
+      if (c >= u.ncols) continue;
+      float m = -INFINITY, l = 0.f;
+      float2 ml[kLatCombFew];
+      float4 x[kLatCombFew], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kLatCombFew; ++i)
+        if (i < u.n) {
+          ml[i] = a.ml[slot(i) + c];
+          x[i] = *reinterpret_cast<const float4*>(a.part + (slot(i) + c) * kLatDim + d);
+          m = fmaxf(m, ml[i].x);
+        }
+      if (m == -INFINITY) m = 0.f;  // no token is visible: every piece's sums are 0
+#pragma unroll
+      for (int i = 0; i < kLatCombFew; ++i)
+        if (i < u.n) {
+          const float e = tc::ex2(ml[i].x - m);
+          l = fmaf(e, ml[i].y, l);
+          acc.x = fmaf(e, x[i].x, acc.x);
+          acc.y = fmaf(e, x[i].y, acc.y);
+          acc.z = fmaf(e, x[i].z, acc.z);
+          acc.w = fmaf(e, x[i].w, acc.w);
+        }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+      store4(a.o + (size_t)(u.col0 + c) * kLatDim + d, o);
+      if (d == 0) a.lse[u.col0 + c] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      continue;
+    }
+    const int c = k >> 2, d = 128 * (k & 3) + 4 * lane;
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < u.n; i += 32) m = fmaxf(m, a.ml[slot(i) + c].x);
+#pragma unroll
+    for (int e = 16; e; e >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
+    if (m == -INFINITY) m = 0.f;
+    for (int i = lane; i < u.n; i += 32) {
+      const float2 ml = a.ml[slot(i) + c];
+      const float e = tc::ex2(ml.x - m);
+      if (w == 0) f[i] = e;
+      l = fmaf(e, ml.y, l);
+    }
+#pragma unroll
+    for (int e = 16; e; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 5
+    for (int i = w; i < u.n; i += kLatCombThreads / 32) {
+      const float4 x = *reinterpret_cast<const float4*>(a.part + (slot(i) + c) * kLatDim + d);
+      const float e = f[i];
+      acc.x = fmaf(e, x.x, acc.x);
+      acc.y = fmaf(e, x.y, acc.y);
+      acc.z = fmaf(e, x.z, acc.z);
+      acc.w = fmaf(e, x.w, acc.w);
+    }
+    acc_s[tid] = acc;
+    __syncthreads();
+    if (w == 0) {
+#pragma unroll
+      for (int i = 1; i < kLatCombThreads / 32; ++i) {
+        const float4 x = acc_s[32 * i + lane];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+      store4(a.o + (size_t)(u.col0 + c) * kLatDim + d, o);
+      if (d == 0) a.lse[u.col0 + c] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+    __syncthreads();  // f and acc_s are free again
+  }
 }
 
 }  // namespace tpc

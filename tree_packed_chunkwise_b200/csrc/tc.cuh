@@ -197,6 +197,11 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 // waits until this thread's committed bulk stores are complete (visible in global memory)
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// fetches a tensor map (a __grid_constant__ parameter) ahead of its first use
+__device__ __forceinline__ void prefetch_tensor_map(const void* tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
+}
+
 // Tiled TMA load (2-D tensor map, no multicast) into this CTA's shared memory; the innermost
 // coordinate x must be a multiple of 8 elements for bf16 (16 bytes).
 __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int x, int y, uint64_t* bar) {
