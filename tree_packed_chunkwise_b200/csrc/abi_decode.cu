@@ -49,7 +49,8 @@ int cache_check(const char* call, const tpc_latent_cache* c, tpc::LatentCache* o
 
 int heads_check(const char* call, int32_t H, int64_t n_rows) {
   if (H < 1 || H > kLatMaxH) return fail(TPC_ERR_UNSUPPORTED, std::string(call) + ": 1 <= H <= 128");
-  if (n_rows * H > INT32_MAX) return fail(TPC_ERR_BAD_SHAPE, std::string(call) + ": more than 2^31 - 1 (row, head) pairs");
+  // (room for a column tile past the end)
+  if (n_rows * H > INT32_MAX - 256) return fail(TPC_ERR_BAD_SHAPE, std::string(call) + ": more than 2^31 - 257 (row, head) pairs");
   return TPC_OK;
 }
 }  // namespace
@@ -160,7 +161,7 @@ int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t
     return fail(TPC_ERR_CUDA, "latent attention: cuTensorMapEncodeTiled failed");
   char* sc = static_cast<char*>(scratch);
   const tpc::LatAttnArgs a{lc, r, H, scale * 1.4426950408889634f, (bf*)o, lse, (float*)sc, (float2*)(sc + tpc::kLatPartBytes),
-                           (tpc::LatPiece*)(sc + tpc::kLatPartBytes + tpc::kLatMlBytes), status, 1};
+                           (tpc::LatPiece*)(sc + tpc::kLatPartBytes + tpc::kLatMlBytes), status};
   const int grid = std::min(tpc_abi::sm_count(), tpc::kLatMaxCtas);
   auto go = [&](auto nt) -> int {
     constexpr int N = decltype(nt)::value;

@@ -41,9 +41,9 @@ static_assert(LatSmem<64>::total <= 232448 && LatSmem<32>::total <= 232448 && La
 
 // scratch: partial sums of the pieces (two per CTA), their (max, sum), and one record per CTA
 struct LatPiece {
-  long long col0;  // first (row, head) pair of the split unit that starts in this CTA
+  int col0;  // first (row, head) pair of the split unit that starts in this CTA
   int ncols;
-  int n;           // its pieces: this CTA's last one, then the first ones of the next n - 1 CTAs
+  int n;     // its pieces: this CTA's last one, then the first ones of the next n - 1 CTAs
 };
 constexpr size_t kLatPartBytes = (size_t)kLatMaxCtas * 2 * kLatMaxNT * kLatDim * 4;
 constexpr size_t kLatMlBytes = (size_t)kLatMaxCtas * 2 * kLatMaxNT * 8;
@@ -60,7 +60,6 @@ struct LatAttnArgs {
   float2* ml;
   LatPiece* meta;
   int* status;
-  int min_tiles;
 };
 
 struct LatSeq {
@@ -71,12 +70,12 @@ __device__ __forceinline__ LatSeq lat_seq(const LatAttnArgs& a, int b) {
   LatSeq s;
   s.row0 = a.rows.row_start ? a.rows.row_start[b] : b;
   const int end = a.rows.row_start ? a.rows.row_start[b + 1] : b + 1;
+  s.kv = max(a.rows.kv_len[b], 0);
   s.m = end - s.row0;
   if (s.row0 < 0 || end < s.row0 || end > a.rows.n_rows) {
     set_status(a.status, kStatusCheck);
     s.row0 = s.m = 0;
   }
-  s.kv = max(a.rows.kv_len[b], 0);
   const int cap = a.cache.max_pages * a.cache.page_size;
   if (s.kv > cap && s.m > 0) set_status(a.status, kStatusCheck);
   s.kv = min(s.kv, cap);
@@ -86,12 +85,12 @@ __device__ __forceinline__ LatSeq lat_seq(const LatAttnArgs& a, int b) {
 // column tiles of a sequence
 template <int NT>
 __device__ __forceinline__ int lat_cts(const LatAttnArgs& a, const LatSeq& s) {
-  return (int)(((long long)s.m * a.H + NT - 1) / NT);
+  return (s.m * a.H + NT - 1) / NT;
 }
 // token tiles that the columns of column tile ct can see (at least one: the rows are written either way)
 template <int NT>
 __device__ __forceinline__ int lat_tiles(const LatAttnArgs& a, const LatSeq& s, int ct) {
-  const int last = min((int)(((long long)(ct + 1) * NT - 1) / a.H), s.m - 1);
+  const int last = s.m == 1 ? 0 : min(((ct + 1) * NT - 1) / a.H, s.m - 1);
   return max(1, (s.kv - s.m + last + kLatKT) / kLatKT);
 }
 
@@ -220,13 +219,15 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     prefetch_tensor_map(&tma_q);
   }
 
-  // ---- this CTA's share
+  // ---- this CTA's share: every thread sums the tiles of consecutive sequences
   const int lo = (int)((long long)a.rows.n_seqs * tid / kLatAttnThreads);
   const int hi = (int)((long long)a.rows.n_seqs * (tid + 1) / kLatAttnThreads);
   long long mine = 0;
+#pragma unroll 1
   for (int b = lo; b < hi; ++b) {
     const LatSeq s = lat_seq(a, b);
     const int n = lat_cts<NT>(a, s);
+#pragma unroll 1
     for (int c = 0; c < n; ++c) mine += lat_tiles<NT>(a, s, c);
   }
   long long incl = mine;
@@ -259,14 +260,15 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     if (i < w) incl += sums[i];
     total += sums[i];
   }
-  long long per = total <= INT32_MAX ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
-  per = max(per, (long long)a.min_tiles);
+  const long long per = total <= INT32_MAX ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
   const long long start = per * blockIdx.x, share = max(0ll, min(per, total - start));
   if (share > 0 && start >= incl - mine && start < incl) {
     long long at = start - (incl - mine);
+#pragma unroll 1
     for (int b = lo; b < hi; ++b) {
       const LatSeq s = lat_seq(a, b);
       const int n = lat_cts<NT>(a, s);
+#pragma unroll 1
       for (int c = 0; c < n; ++c) {
         const int t = lat_tiles<NT>(a, s, c);
         if (at >= 0 && at < t) {
@@ -401,7 +403,8 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     auto sum_now = [&] {
       if (pend >= 0 && __all_sync(0xffffffffu, wait(&p_full[pend & 1], (pend >> 1) & 1))) weighted_sum();
     };
-    for (; walk.left > 0; walk.next(), ++piece) {
+    // (loop bounds read from one lane: the compiler then knows that the warp agrees on them)
+    for (; __shfl_sync(0xffffffffu, walk.left > 0, 0); walk.next(), ++piece) {
       wait_or_sum(q_full, piece & 1);
       const int n = __shfl_sync(0xffffffffu, walk.n, 0);
       for (int i = 0; i < n; ++i, ++it) {
@@ -447,11 +450,10 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     if (st == 0) a.meta[blockIdx.x].n = 0;
     for (; walk.left > 0; walk.next()) {
       const LatSeq s = walk.s;
-      const long long col0 = (long long)s.row0 * a.H + (long long)walk.ct * NT;
-      const int ncols = (int)min((long long)NT, (long long)s.m * a.H - (long long)walk.ct * NT);
+      const int col0 = s.row0 * a.H + walk.ct * NT, ncols = min(NT, s.m * a.H - walk.ct * NT);
       // last visible position of every column (columns past the run's end take its last row's)
-      if (st < NT) lim[st] = s.kv - s.m + min((int)(((long long)walk.ct * NT + st) / a.H), s.m - 1);
-      const int lim0 = s.kv - s.m + (int)((long long)walk.ct * NT / a.H);
+      if (st < NT) lim[st] = s.kv - s.m + min((walk.ct * NT + st) / a.H, s.m - 1);
+      const int lim0 = s.kv - s.m + walk.ct * NT / a.H;
       float mx[2 * R], sum[2 * R];
 #pragma unroll
       for (int c = 0; c < 2 * R; ++c) {
@@ -617,7 +619,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
         if (whole) {
 #pragma unroll
           for (int c = 0; c < 16; ++c)
-            if (cc + c < ncols) a.o[(size_t)(col0 + cc + c) * kLatDim + dim] = __float2bfloat16_rn(v[c] * fac[cc + c]);
+            if (cc + c < ncols) a.o[((size_t)col0 + cc + c) * kLatDim + dim] = __float2bfloat16_rn(v[c] * fac[cc + c]);
         } else {
 #pragma unroll
           for (int c = 0; c < 16; ++c)
@@ -698,7 +700,7 @@ __global__ void __launch_bounds__(kLatCombThreads) latent_combine_kernel(LatAttn
         }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-      store4(a.o + (size_t)(u.col0 + c) * kLatDim + d, o);
+      store4(a.o + ((size_t)u.col0 + c) * kLatDim + d, o);
       if (d == 0) a.lse[u.col0 + c] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       continue;
     }
@@ -740,7 +742,7 @@ __global__ void __launch_bounds__(kLatCombThreads) latent_combine_kernel(LatAttn
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-      store4(a.o + (size_t)(u.col0 + c) * kLatDim + d, o);
+      store4(a.o + ((size_t)u.col0 + c) * kLatDim + d, o);
       if (d == 0) a.lse[u.col0 + c] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
     __syncthreads();  // f and acc_s are free again
