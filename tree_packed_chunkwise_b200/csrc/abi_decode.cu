@@ -15,6 +15,8 @@ using tpc_abi::fail;
 using tpc_abi::g_prof;
 using tpc_abi::set_smem;
 using tpc_abi::tensor_map;
+using tpc_abi::tensor_map_rows;
+using tpc_abi::tensor_map_rows_ld;
 using bf = __nv_bfloat16;
 
 static_assert(TPC_LATENT_DIM == tpc::kLatDim && TPC_LATENT_ROPE == tpc::kLatRope && TPC_LATENT_HEAD == tpc::kLatHead &&
@@ -130,9 +132,18 @@ int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld
     return fail(TPC_ERR_BAD_SHAPE, "latent absorb: 16-byte aligned tensors, ld_q >= 192 H and a multiple of 8");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   tpc_abi::NvtxRange nvtx_call("tpc_latent_absorb");
-  const unsigned grid = (unsigned)((int64_t)r.n_rows * H);
-  TPC_LAUNCH("latent_absorb", st, (tpc::latent_absorb_kernel<<<grid, tpc::kHeadThreads, 0, st>>>(
-                                      r, H, (const bf*)q, ld_q, (const bf*)w_b, (bf*)qa)));
+  CUtensorMap tx, tw;
+  if (!tensor_map_rows_ld(&tx, q, tpc::kLatQK, H, r.n_rows, ld_q, 128) ||
+      !tensor_map(&tw, w_b, tpc::kLatDim, (uint64_t)2 * tpc::kLatHead * H, tpc::kLatDim, 64))
+    return fail(TPC_ERR_CUDA, "latent absorb: cuTensorMapEncodeTiled failed");
+  constexpr int BN = 128, per = tpc::kHeadTcThreads / 32;
+  const int rope = (r.n_rows + per - 1) / per;
+  const int64_t grid = rope + (int64_t)((r.n_rows + 127) / 128) * H * (tpc::kLatDim / BN);
+  const tpc::HeadArgs a{r, H, r.n_rows, (const bf*)q, ld_q, (bf*)qa, status, rope};
+  constexpr size_t smem = tpc::HeadSmem<tpc::kAbsorb, BN>::total;
+  TPC_CUDA(set_smem(tpc::latent_head_tc<tpc::kAbsorb, BN>, smem));
+  TPC_LAUNCH("latent_absorb", st,
+             (tpc::latent_head_tc<tpc::kAbsorb, BN><<<(unsigned)grid, tpc::kHeadTcThreads, smem, st>>>(tx, tw, a)));
   return TPC_OK;
 }
 
@@ -194,10 +205,20 @@ int tpc_latent_expand(int32_t n_rows, int32_t H, const void* o, const void* w_b,
   if (misaligned(o) || misaligned(w_b) || misaligned(out)) return fail(TPC_ERR_BAD_SHAPE, "latent expand: tensors must be 16-byte aligned");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   tpc_abi::NvtxRange nvtx_call("tpc_latent_expand");
-  const unsigned grid = (unsigned)((int64_t)n_rows * H);
-  TPC_LAUNCH("latent_expand", st, (tpc::latent_expand_kernel<<<grid, tpc::kHeadThreads, 0, st>>>(
-                                      H, (const bf*)o, (const bf*)w_b, (bf*)out)));
-  return TPC_OK;
+  const tpc::HeadArgs a{{}, H, n_rows, nullptr, 0, (bf*)out, status, 0};
+  const int64_t tiles = (int64_t)((n_rows + 127) / 128) * H;
+  auto go = [&](auto bn) -> int {
+    constexpr int BN = decltype(bn)::value;
+    CUtensorMap tx, tw;
+    if (!tensor_map_rows(&tx, o, tpc::kLatDim, H, n_rows, 128) ||
+        !tensor_map(&tw, w_b, tpc::kLatDim, (uint64_t)2 * tpc::kLatHead * H, tpc::kLatDim, BN))
+      return fail(TPC_ERR_CUDA, "latent expand: cuTensorMapEncodeTiled failed");
+    constexpr size_t smem = tpc::HeadSmem<tpc::kExpand, BN>::total;
+    TPC_CUDA(set_smem(tpc::latent_head_tc<tpc::kExpand, BN>, smem));
+    TPC_LAUNCH("latent_expand", st, (tpc::latent_head_tc<tpc::kExpand, BN><<<(unsigned)(tiles * (tpc::kLatHead / BN)), tpc::kHeadTcThreads, smem, st>>>(tx, tw, a)));
+    return TPC_OK;
+  };
+  return go(std::integral_constant<int, 128>{});
 }
 
 }  // extern "C"

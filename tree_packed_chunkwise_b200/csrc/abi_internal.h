@@ -58,6 +58,9 @@ bool tensor_map(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, u
 // box_rows rows in the 128-byte-swizzled layout; rows past the end read as zeros.
 bool tensor_map_rows(CUtensorMap* m, const void* ptr, uint64_t features, uint64_t heads, uint64_t rows,
                      uint32_t box_rows);
+// the same with ld_elems elements from row to row (a multiple of 8)
+bool tensor_map_rows_ld(CUtensorMap* m, const void* ptr, uint64_t features, uint64_t heads, uint64_t rows,
+                        uint64_t ld_elems, uint32_t box_rows);
 
 // Optional per-kernel timing: CUDA events around every launch (on the launching stream).
 struct Profiler {

@@ -1,5 +1,5 @@
 // Kernels of token-by-token generation: the recurrent KDA step on a cache of states, the append to
-// the paged cache of latents, and the per-head products of latent attention.
+// the paged cache of latents, and the rotation of the absorbed queries.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -272,49 +272,6 @@ __device__ __forceinline__ void absorb_rope_row(const DecodeRows& rows, int H, c
     d[lane] = __float2bfloat16_rn(x * cs - y * sn);
     d[lane + 32] = __float2bfloat16_rn(x * sn + y * cs);
   }
-}
-
-constexpr int kHeadThreads = 128;
-
-// One CTA per (row, head): 512 dot products of 128 terms, thread = 4 neighbouring outputs.
-__global__ void __launch_bounds__(kHeadThreads)
-    latent_absorb_kernel(DecodeRows rows, int H, const __nv_bfloat16* q, int64_t ld_q, const __nv_bfloat16* w_b,
-                         __nv_bfloat16* qa) {
-  __shared__ float x[kLatHead];
-  const int t = (int)(blockIdx.x / H), h = (int)(blockIdx.x % H);
-  if (rows.row_start && (t >= rows.row_start[rows.n_seqs] || t < rows.row_start[0])) return;
-  if (h == 0 && threadIdx.x < 32) absorb_rope_row(rows, H, q, ld_q, qa, t);
-  x[threadIdx.x] = to_f(q[(size_t)t * ld_q + (size_t)h * kLatQK + threadIdx.x]);
-  __syncthreads();
-  float acc[4] = {};
-  const __nv_bfloat16* w = w_b + (size_t)h * kLatHead * kLatDim + 4 * threadIdx.x;
-  for (int i = 0; i < kLatHead; ++i) {
-    float y[4];
-    load_vec<__nv_bfloat16, 4>(w + (size_t)i * kLatDim, y);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = fmaf(x[i], y[j], acc[j]);
-  }
-  store4(qa + ((size_t)t * H + h) * kLatWidth + 4 * threadIdx.x, acc);
-}
-
-// One CTA per (row, head): 128 dot products of 512 terms, thread = output.
-__global__ void __launch_bounds__(kHeadThreads)
-    latent_expand_kernel(int H, const __nv_bfloat16* o, const __nv_bfloat16* w_b, __nv_bfloat16* out) {
-  __shared__ float x[kLatDim];
-  const int t = (int)(blockIdx.x / H), h = (int)(blockIdx.x % H);
-  float y[8];
-  load_vec<__nv_bfloat16, 4>(o + ((size_t)t * H + h) * kLatDim + 4 * threadIdx.x, *reinterpret_cast<float(*)[4]>(y));
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x[4 * threadIdx.x + j] = y[j];
-  __syncthreads();
-  const __nv_bfloat16* w = w_b + ((size_t)(H + h) * kLatHead + threadIdx.x) * kLatDim;
-  float acc = 0.f;
-  for (int i = 0; i < kLatDim; i += 8) {
-    load_vec<__nv_bfloat16, 8>(w + i, y);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc = fmaf(x[i + j], y[j], acc);
-  }
-  out[((size_t)t * H + h) * kLatHead + threadIdx.x] = __float2bfloat16_rn(acc);
 }
 
 }  // namespace tpc

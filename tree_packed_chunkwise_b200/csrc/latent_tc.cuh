@@ -749,4 +749,154 @@ __global__ void __launch_bounds__(kLatCombThreads) latent_combine_kernel(LatAttn
   }
 }
 
+// ------------------------------------------------------------------------------------ per-head products
+// Y[t][h][n] = sum_k X[t][h][k] B_h[k][n] of the absorbed form, one CTA per (128 rows, head, BN outputs):
+//   kAbsorb: X = q_nope (K = 128), B_h = W_k[h] as it is stored ([k][n], MN-major), 512 outputs;
+//   kExpand: X = o (K = 512), B_h = W_v[h]^T (stored [n][k], K-major), 128 outputs.
+// Bound by reading X and writing Y (K is short); the weights and the re-read rows come from L2.  Two or
+// three CTAs share an SM and hide one another's latency, so a CTA does one tile: warp 0 loads K steps
+// of 64 by TMA, warp 1 issues M = 128 MMAs, warps 2-5 round the accumulator to bf16 and write whole
+// 256-byte row pieces through shared memory.
+enum : int { kAbsorb = 0, kExpand = 1 };
+constexpr int kHeadTcThreads = 192;
+
+template <int KIND, int BN>
+struct HeadSmem {
+  static constexpr int K = KIND == kAbsorb ? kLatHead : kLatDim, steps = K / 64, N = KIND == kAbsorb ? kLatDim : kLatHead;
+  static constexpr int stages = KIND == kAbsorb ? 2 : 3;
+  static constexpr uint32_t a = 128 * 128, stage = a + BN * 128, out_ld = BN * 2 + 16;
+  static constexpr uint32_t total = stages * stage + 1024;  // + slack to align the stages to 1024 bytes
+  static_assert(128 * out_ld <= stages * stage, "the output tile takes the stages' place");
+};
+
+struct HeadArgs {
+  DecodeRows rows;  // kAbsorb: positions, and the rows that belong to a sequence
+  int H, n_rows;
+  const __nv_bfloat16* q;  // kAbsorb: rotary part
+  int64_t ld_q;
+  __nv_bfloat16* y;
+  int* status;
+  int rope_ctas;  // leading CTAs that turn the rotary parts (kAbsorb)
+};
+
+template <int KIND, int BN>
+__global__ void __launch_bounds__(kHeadTcThreads)
+    latent_head_tc(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, HeadArgs a) {
+  using namespace tc;
+  using L = HeadSmem<KIND, BN>;
+  extern __shared__ __align__(1024) uint8_t hsm_raw[];
+  uint8_t* sm = hsm_raw + ((1024u - (smem_u32(hsm_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) uint64_t full[L::stages], empty[L::stages], acc_full;
+  __shared__ uint32_t tslot;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  if constexpr (KIND == kAbsorb) {
+    if ((int)blockIdx.x < a.rope_ctas) {
+      const int64_t t = (int64_t)blockIdx.x * (kHeadTcThreads / 32) + w;
+      if (t < a.n_rows) absorb_rope_row(a.rows, a.H, a.q, a.ld_q, a.y, (int)t);
+      return;
+    }
+  }
+  // tile order: output blocks, then heads, fastest, so that CTAs in flight read the same rows
+  int tile = (int)blockIdx.x - a.rope_ctas;
+  const int n0 = tile % (L::N / BN) * BN;
+  tile /= L::N / BN;
+  const int h = tile % a.H, t0 = tile / a.H * 128;
+  if (tid == 0) {
+    prefetch_tensor_map(&tma_x);
+    prefetch_tensor_map(&tma_w);
+    for (int i = 0; i < L::stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&acc_full, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (w == 1) tmem_alloc(&tslot, BN);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tb = tslot;
+  // every wait is bounded; a role whose wait ran out records it and goes on without the data
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_wait(bar, parity, 2000000000ull)) return true;
+    set_status(a.status, 8);
+    return false;
+  };
+  if (w == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (; issued < L::steps; ++issued) {
+        const int st = issued % L::stages, k0 = 64 * issued;
+        if (issued >= L::stages && !wait(&empty[st], (issued / L::stages - 1) & 1)) break;
+        uint8_t* xs = sm + st * L::stage;
+        mbar_arrive_expect_tx(&full[st], L::stage);
+        tma_load_3d(xs, &tma_x, k0, h, t0, &full[st]);
+        if constexpr (KIND == kAbsorb) {
+          for (int j = 0; j < BN / 64; ++j)
+            tma_load_2d(xs + L::a + j * 64 * 128, &tma_w, n0 + 64 * j, h * kLatHead + k0, &full[st]);
+        } else {
+          tma_load_2d(xs + L::a, &tma_w, k0, (a.H + h) * kLatHead + n0, &full[st]);
+        }
+      }
+      if (issued < L::steps)  // copies in flight land before the CTA ends
+        for (int i = max(0, issued - L::stages); i < issued; ++i) mbar_wait(&full[i % L::stages], (i / L::stages) & 1, 100000000ull);
+    }
+  } else if (w == 1) {
+    const uint32_t lead = elect_one();
+    constexpr uint32_t id = idesc_bf16(128, BN, false, KIND == kAbsorb);
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < L::steps; ++i) {
+      const int st = i % L::stages;
+      ok = ok && __all_sync(0xffffffffu, wait(&full[st], (i / L::stages) & 1));
+      if (!ok) break;
+      fence_after_sync();
+      const uint32_t xs = smem_u32(sm) + st * L::stage;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mma_bf16_if(lead, tb, sw_desc_k(xs, 128, ks),
+                    KIND == kAbsorb ? sw_desc_mn(xs + L::a, 64, ks) : sw_desc_k(xs + L::a, BN, ks), id, i || ks ? 1u : 0u);
+      commit_if(lead, &empty[st]);
+    }
+    commit_if(lead, &acc_full);
+    wait(&acc_full, 0);
+    __syncwarp();
+  } else {
+    const int sp = w & 3;
+    const bool got = __all_sync(0xffffffffu, wait(&acc_full, 0));
+    fence_after_sync();
+    int first = 0, last = a.n_rows;  // rows that belong to a sequence
+    if (KIND == kAbsorb && a.rows.row_start) {
+      first = a.rows.row_start[0];
+      last = min(last, a.rows.row_start[a.rows.n_seqs]);
+    }
+    uint8_t* out = sm + 32 * sp * L::out_ld;  // this warp's rows; every copy has landed and been read
+#pragma unroll
+    for (int c0 = 0; c0 < BN; c0 += 32) {
+      uint32_t r[32];
+      tmem_ld32_nowait(tb + ((uint32_t)(32 * sp) << 16) + c0, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+#pragma unroll
+      for (int i = 0; i < 32; i += 8)
+        *reinterpret_cast<uint4*>(out + lane * L::out_ld + (c0 + i) * 2) = make_uint4(
+            pack_bf16(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), pack_bf16(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])),
+            pack_bf16(__uint_as_float(r[i + 4]), __uint_as_float(r[i + 5])), pack_bf16(__uint_as_float(r[i + 6]), __uint_as_float(r[i + 7])));
+    }
+    __syncwarp();
+    constexpr int lanes = BN / 8, at_once = 32 / lanes, width = KIND == kAbsorb ? kLatWidth : kLatHead;
+#pragma unroll 4
+    for (int i = lane / lanes; i < 32; i += at_once) {
+      const int t = t0 + 32 * sp + i;
+      if (got && t >= first && t < last)
+        *reinterpret_cast<uint4*>(a.y + ((size_t)t * a.H + h) * width + n0 + lane % lanes * 8) =
+            *reinterpret_cast<const uint4*>(out + i * L::out_ld + lane % lanes * 16);
+    }
+    fence_before_sync();
+  }
+  __syncthreads();
+  if (w == 1) tmem_dealloc(tb, BN);
+}
+
 }  // namespace tpc

@@ -76,10 +76,15 @@ bool tensor_map(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, u
 // end read as zeros.
 bool tensor_map_rows(CUtensorMap* m, const void* ptr, uint64_t features, uint64_t heads, uint64_t rows,
                      uint32_t box_rows) {
+  return tensor_map_rows_ld(m, ptr, features, heads, rows, heads * features, box_rows);
+}
+
+bool tensor_map_rows_ld(CUtensorMap* m, const void* ptr, uint64_t features, uint64_t heads, uint64_t rows,
+                        uint64_t ld_elems, uint32_t box_rows) {
   const auto enc = encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {features, heads, rows};
-  cuuint64_t strides[2] = {features * 2, heads * features * 2};
+  cuuint64_t strides[2] = {features * 2, ld_elems * 2};
   cuuint32_t box[3] = {64, 1, box_rows};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
