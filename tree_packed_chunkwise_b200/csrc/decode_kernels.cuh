@@ -257,20 +257,35 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendArg
 }
 
 // ------------------------------------------------------------------------------------ rotated queries
-// The rotary part of the absorbed queries: a warp turns every head of one row (lane i: the pair i, i + 32).
+// The rotary part of the absorbed queries: a warp turns every head of one row.  Lane i takes cos and sin of
+// angle i; then four lanes hold a head (8 neighbouring pairs each), eight heads at a time.
 __device__ __forceinline__ void absorb_rope_row(const DecodeRows& rows, int H, const __nv_bfloat16* q, int64_t ld_q,
                                                 __nv_bfloat16* qa, int t) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, j0 = (lane & 3) * 8;
   const RowAt r = row_at(rows, t);
   if (r.seq < 0) return;
-  float cs, sn;
+  float cs, sn, c[8], s[8];
   rope_angle(r.pos, lane, &cs, &sn);
-  for (int h = 0; h < H; ++h) {
-    const __nv_bfloat16* s = q + (size_t)t * ld_q + (size_t)h * kLatQK + kLatHead;
-    __nv_bfloat16* d = qa + ((size_t)t * H + h) * kLatWidth + kLatDim;
-    const float x = to_f(s[lane]), y = to_f(s[lane + 32]);
-    d[lane] = __float2bfloat16_rn(x * cs - y * sn);
-    d[lane + 32] = __float2bfloat16_rn(x * sn + y * cs);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    c[j] = __shfl_sync(0xffffffffu, cs, j0 + j);
+    s[j] = __shfl_sync(0xffffffffu, sn, j0 + j);
+  }
+#pragma unroll 2
+  for (int h = lane >> 2; h < H; h += 8) {
+    const __nv_bfloat16* src = q + (size_t)t * ld_q + (size_t)h * kLatQK + kLatHead + j0;
+    __nv_bfloat16* dst = qa + ((size_t)t * H + h) * kLatWidth + kLatDim + j0;
+    float x[8], y[8];
+    load_vec<__nv_bfloat16, 8>(src, x);
+    load_vec<__nv_bfloat16, 8>(src + 32, y);
+    __align__(16) __nv_bfloat16 u[8], v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      u[j] = __float2bfloat16_rn(x[j] * c[j] - y[j] * s[j]);
+      v[j] = __float2bfloat16_rn(x[j] * s[j] + y[j] * c[j]);
+    }
+    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(u);
+    *reinterpret_cast<uint4*>(dst + 32) = *reinterpret_cast<const uint4*>(v);
   }
 }
 
