@@ -15,6 +15,7 @@ using tpc_abi::fail;
 using tpc_abi::g_prof;
 using tpc_abi::set_smem;
 using tpc_abi::tensor_map;
+using tpc_abi::tensor_map_f32;
 using tpc_abi::tensor_map_rows;
 using tpc_abi::tensor_map_rows_ld;
 using bf = __nv_bfloat16;
@@ -68,23 +69,41 @@ int tpc_kda_step(const tpc_kda_shape* shape, const tpc_rows* rows, const tpc_kda
   if (shape->dk != 32 && shape->dk != 64 && shape->dk != 128) return fail(TPC_ERR_UNSUPPORTED, "kda step: head size 32, 64 or 128");
   if ((shape->in_dtype != TPC_F32 && shape->in_dtype != TPC_BF16) || (shape->out_dtype != TPC_F32 && shape->out_dtype != TPC_BF16))
     return fail(TPC_ERR_UNSUPPORTED, "kda step: dtypes are TPC_F32 or TPC_BF16");
-  if (io->n_slots < 0) return fail(TPC_ERR_BAD_SHAPE, "kda step: negative n_slots");
+  if (io->n_slots < 1) return fail(TPC_ERR_BAD_SHAPE, "kda step: n_slots must be >= 1");
   if (r.n_seqs == 0) return TPC_OK;
-  if (!io->src || (io->n_slots > 0 && !io->state)) return fail(TPC_ERR_NULL, "kda step: state or src is NULL");
+  if (!io->src || !io->state) return fail(TPC_ERR_NULL, "kda step: state or src is NULL");
   if (r.n_rows > 0 && (!io->q || !io->k || !io->v || !io->g || !io->beta || !io->o))
     return fail(TPC_ERR_NULL, "kda step: NULL tensor");
   for (const void* p : {io->q, io->k, io->v, io->g, (const void*)io->state, (const void*)io->o})
     if (misaligned(p)) return fail(TPC_ERR_BAD_SHAPE, "kda step: tensors must be 16-byte aligned");
-  const int64_t warps = (int64_t)r.n_seqs * shape->H * (shape->dk / 8), per = tpc::kStepThreads / 32;
-  const int64_t grid = (warps + per - 1) / per;
-  if (grid > INT32_MAX) return fail(TPC_ERR_BAD_SHAPE, "kda step: too many sequences and heads");
+  if ((int64_t)io->n_slots * shape->H * shape->dk > INT32_MAX || (int64_t)r.n_seqs * shape->H > INT32_MAX)
+    return fail(TPC_ERR_BAD_SHAPE, "kda step: more than 2^31 - 1 state rows (n_slots * H * d) or heads (n_seqs * H)");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   tpc_abi::NvtxRange nvtx_call("tpc_kda_step");
   const tpc::StepArgs a{io->q, io->k, io->v, io->g, io->beta, io->state, io->src, io->dst, io->o, io->n_slots, shape->H, r, status};
+  // the ring pays once its units give every SM one and the rows are single tokens (both sides at the kernels)
+  const int64_t heads = (int64_t)r.n_seqs * shape->H;
+  const bool ring = shape->dk == 128 && r.n_rows <= r.n_seqs && heads >= 128;
+  CUtensorMap ts;
+  if (ring && !tensor_map_f32(&ts, io->state, 128, (uint64_t)io->n_slots * shape->H * 128, tpc::kStepCols, 128))
+    return fail(TPC_ERR_CUDA, "kda step: cuTensorMapEncodeTiled failed");
+  const int64_t units = heads * (128 / tpc::kStepCols), warps = heads * (shape->dk * shape->dk / 1024);
+  const unsigned ring_grid = (unsigned)std::min<int64_t>(units, (int64_t)tpc::kStepPerSm * tpc_abi::sm_count());
+  constexpr int per = tpc::kStepThreads / 32;
+  if ((warps + per - 1) / per > INT32_MAX) return fail(TPC_ERR_BAD_SHAPE, "kda step: too many sequences and heads");
+  const unsigned grid = (unsigned)((warps + per - 1) / per);
   auto go = [&](auto tin, auto tout, auto d) -> int {
     using T = decltype(tin);
     using TO = decltype(tout);
-    TPC_LAUNCH("kda_step", st, (tpc::kda_step_kernel<T, TO, decltype(d)::value><<<(unsigned)grid, tpc::kStepThreads, 0, st>>>(a)));
+    constexpr int D = decltype(d)::value;
+    if constexpr (D == 128)
+      if (ring) {
+        constexpr size_t smem = tpc::StepSmem<D>::total;
+        TPC_CUDA(set_smem(tpc::kda_step_ring<T, TO, D>, smem));
+        TPC_LAUNCH("kda_step_ring", st, (tpc::kda_step_ring<T, TO, D><<<ring_grid, tpc::kStepThreads, smem, st>>>(ts, a)));
+        return TPC_OK;
+      }
+    TPC_LAUNCH("kda_step_regs", st, (tpc::kda_step_regs<T, TO, D><<<grid, tpc::kStepThreads, 0, st>>>(a)));
     return TPC_OK;
   };
   auto with_d = [&](auto tin, auto tout) -> int {
