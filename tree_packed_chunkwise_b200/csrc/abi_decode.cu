@@ -15,7 +15,6 @@ using tpc_abi::fail;
 using tpc_abi::g_prof;
 using tpc_abi::set_smem;
 using tpc_abi::tensor_map;
-using tpc_abi::tensor_map_f32;
 using tpc_abi::tensor_map_rows;
 using tpc_abi::tensor_map_rows_ld;
 using bf = __nv_bfloat16;
@@ -76,34 +75,18 @@ int tpc_kda_step(const tpc_kda_shape* shape, const tpc_rows* rows, const tpc_kda
     return fail(TPC_ERR_NULL, "kda step: NULL tensor");
   for (const void* p : {io->q, io->k, io->v, io->g, (const void*)io->state, (const void*)io->o})
     if (misaligned(p)) return fail(TPC_ERR_BAD_SHAPE, "kda step: tensors must be 16-byte aligned");
-  if ((int64_t)io->n_slots * shape->H * shape->dk > INT32_MAX || (int64_t)r.n_seqs * shape->H > INT32_MAX)
-    return fail(TPC_ERR_BAD_SHAPE, "kda step: more than 2^31 - 1 state rows (n_slots * H * d) or heads (n_seqs * H)");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  tpc_abi::NvtxRange nvtx_call("tpc_kda_step");
   const tpc::StepArgs a{io->q, io->k, io->v, io->g, io->beta, io->state, io->src, io->dst, io->o, io->n_slots, shape->H, r, status};
-  // the ring pays once its units give every SM one and the rows are single tokens (both sides at the kernels)
-  const int64_t heads = (int64_t)r.n_seqs * shape->H;
-  const bool ring = shape->dk == 128 && r.n_rows <= r.n_seqs && heads >= 128;
-  CUtensorMap ts;
-  if (ring && !tensor_map_f32(&ts, io->state, 128, (uint64_t)io->n_slots * shape->H * 128, tpc::kStepCols, 128))
-    return fail(TPC_ERR_CUDA, "kda step: cuTensorMapEncodeTiled failed");
-  const int64_t units = heads * (128 / tpc::kStepCols), warps = heads * (shape->dk * shape->dk / 1024);
-  const unsigned ring_grid = (unsigned)std::min<int64_t>(units, (int64_t)tpc::kStepPerSm * tpc_abi::sm_count());
   constexpr int per = tpc::kStepThreads / 32;
-  if ((warps + per - 1) / per > INT32_MAX) return fail(TPC_ERR_BAD_SHAPE, "kda step: too many sequences and heads");
-  const unsigned grid = (unsigned)((warps + per - 1) / per);
+  if ((int64_t)r.n_seqs * shape->H > INT32_MAX / per) return fail(TPC_ERR_BAD_SHAPE, "kda step: too many sequences and heads");
+  tpc_abi::NvtxRange nvtx_call("tpc_kda_step");
   auto go = [&](auto tin, auto tout, auto d) -> int {
     using T = decltype(tin);
     using TO = decltype(tout);
     constexpr int D = decltype(d)::value;
-    if constexpr (D == 128)
-      if (ring) {
-        constexpr size_t smem = tpc::StepSmem<D>::total;
-        TPC_CUDA(set_smem(tpc::kda_step_ring<T, TO, D>, smem));
-        TPC_LAUNCH("kda_step_ring", st, (tpc::kda_step_ring<T, TO, D><<<ring_grid, tpc::kStepThreads, smem, st>>>(ts, a)));
-        return TPC_OK;
-      }
-    TPC_LAUNCH("kda_step_regs", st, (tpc::kda_step_regs<T, TO, D><<<grid, tpc::kStepThreads, 0, st>>>(a)));
+    const int64_t warps = (int64_t)r.n_seqs * shape->H * tpc::StepShape<D>::warps;
+    TPC_LAUNCH("kda_step", st,
+               (tpc::kda_step_kernel<T, TO, D><<<(unsigned)((warps + per - 1) / per), tpc::kStepThreads, 0, st>>>(a)));
     return TPC_OK;
   };
   auto with_d = [&](auto tin, auto tout) -> int {
@@ -155,14 +138,13 @@ int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld
   if (!tensor_map_rows_ld(&tx, q, tpc::kLatQK, H, r.n_rows, ld_q, 128) ||
       !tensor_map(&tw, w_b, tpc::kLatDim, (uint64_t)2 * tpc::kLatHead * H, tpc::kLatDim, 64))
     return fail(TPC_ERR_CUDA, "latent absorb: cuTensorMapEncodeTiled failed");
-  constexpr int BN = 128, per = tpc::kHeadTcThreads / 32;
-  const int rope = (r.n_rows + per - 1) / per;
-  const int64_t grid = rope + (int64_t)((r.n_rows + 127) / 128) * H * (tpc::kLatDim / BN);
-  const tpc::HeadArgs a{r, H, r.n_rows, (const bf*)q, ld_q, (bf*)qa, status, rope};
-  constexpr size_t smem = tpc::HeadSmem<tpc::kAbsorb, BN>::total;
-  TPC_CUDA(set_smem(tpc::latent_head_tc<tpc::kAbsorb, BN>, smem));
-  TPC_LAUNCH("latent_absorb", st,
-             (tpc::latent_head_tc<tpc::kAbsorb, BN><<<(unsigned)grid, tpc::kHeadTcThreads, smem, st>>>(tx, tw, a)));
+  const int64_t tiles = (int64_t)((r.n_rows + 127) / 128) * H;
+  const int sms = tpc_abi::sm_count(), blocks = tiles >= 2 * sms ? 4 : 2 * tiles >= sms ? 2 : 1;  // measured at the kernel
+  const int64_t grid = tiles * (4 / blocks);
+  const tpc::AbsorbArgs a{r, H, (const bf*)q, ld_q, (bf*)qa, status, blocks};
+  constexpr size_t smem = tpc::AbsorbSmem::total;
+  TPC_CUDA(set_smem(tpc::latent_absorb_tc, smem));
+  TPC_LAUNCH("latent_absorb_tc", st, (tpc::latent_absorb_tc<<<(unsigned)grid, tpc::kHeadTcThreads, smem, st>>>(tx, tw, a)));
   return TPC_OK;
 }
 
@@ -224,20 +206,16 @@ int tpc_latent_expand(int32_t n_rows, int32_t H, const void* o, const void* w_b,
   if (misaligned(o) || misaligned(w_b) || misaligned(out)) return fail(TPC_ERR_BAD_SHAPE, "latent expand: tensors must be 16-byte aligned");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   tpc_abi::NvtxRange nvtx_call("tpc_latent_expand");
-  const tpc::HeadArgs a{{}, H, n_rows, nullptr, 0, (bf*)out, status, 0};
-  const int64_t tiles = (int64_t)((n_rows + 127) / 128) * H;
-  auto go = [&](auto bn) -> int {
-    constexpr int BN = decltype(bn)::value;
-    CUtensorMap tx, tw;
-    if (!tensor_map_rows(&tx, o, tpc::kLatDim, H, n_rows, 128) ||
-        !tensor_map(&tw, w_b, tpc::kLatDim, (uint64_t)2 * tpc::kLatHead * H, tpc::kLatDim, BN))
-      return fail(TPC_ERR_CUDA, "latent expand: cuTensorMapEncodeTiled failed");
-    constexpr size_t smem = tpc::HeadSmem<tpc::kExpand, BN>::total;
-    TPC_CUDA(set_smem(tpc::latent_head_tc<tpc::kExpand, BN>, smem));
-    TPC_LAUNCH("latent_expand", st, (tpc::latent_head_tc<tpc::kExpand, BN><<<(unsigned)(tiles * (tpc::kLatHead / BN)), tpc::kHeadTcThreads, smem, st>>>(tx, tw, a)));
-    return TPC_OK;
-  };
-  return go(std::integral_constant<int, 128>{});
+  CUtensorMap tx, tw;
+  if (!tensor_map_rows(&tx, o, tpc::kLatDim, H, n_rows, 128) ||
+      !tensor_map(&tw, w_b, tpc::kLatDim, (uint64_t)2 * tpc::kLatHead * H, tpc::kLatDim, 128))
+    return fail(TPC_ERR_CUDA, "latent expand: cuTensorMapEncodeTiled failed");
+  const tpc::ExpandArgs a{H, n_rows, (bf*)out, status};
+  const unsigned grid = (unsigned)((int64_t)((n_rows + 127) / 128) * H);
+  constexpr size_t smem = tpc::ExpandSmem::total;
+  TPC_CUDA(set_smem(tpc::latent_expand_tc, smem));
+  TPC_LAUNCH("latent_expand_tc", st, (tpc::latent_expand_tc<<<grid, tpc::kHeadTcThreads, smem, st>>>(tx, tw, a)));
+  return TPC_OK;
 }
 
 }  // extern "C"

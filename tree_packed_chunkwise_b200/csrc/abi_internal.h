@@ -54,9 +54,6 @@ int sm_count();
 // 2-D bf16 TMA tensor map over [rows][cols] (leading dimension ld_elems): boxes of 64 columns x
 // box_rows rows, each box row one 128-byte swizzled line.
 bool tensor_map(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld_elems, uint32_t box_rows);
-// 2-D fp32 TMA tensor map over a contiguous [rows][cols] matrix: boxes of box_cols columns x box_rows
-// rows, rows back to back in shared memory (no swizzle).
-bool tensor_map_f32(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows);
 // 3-D bf16 TMA tensor map over a [rows][heads][features] tensor: boxes of 64 features x 1 head x
 // box_rows rows in the 128-byte-swizzled layout; rows past the end read as zeros.
 bool tensor_map_rows(CUtensorMap* m, const void* ptr, uint64_t features, uint64_t heads, uint64_t rows,

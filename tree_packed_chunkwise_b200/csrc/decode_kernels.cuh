@@ -1,13 +1,11 @@
 // Kernels of token-by-token generation: the recurrent KDA step on a cache of states, the append to
 // the paged cache of latents, and the rotation of the absorbed queries.
 #pragma once
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
 #include "common.cuh"
-#include "tc.cuh"
 
 namespace tpc {
 
@@ -117,13 +115,21 @@ constexpr int kStepThreads = 128;
 // so one pass over a column does everything: a state is read once and written once, and their bytes
 // bound the step (4 flops a byte).
 //
-// In registers: a warp owns 256 / D groups of 4 columns, a lane 8 rows x 4 columns; sums over the rows are
-// shuffles, and nothing is shared between warps (no barrier).  For small batches and runs of rows
-// (launch and latency bound; 16 heads of one sequence 2.8 us against 3.4 us of the kernel below, runs of
-// six rows 52 against 58 us) and for d < 128.
+// A lane holds R rows x 4 columns of one head's state in registers, a warp 4 CG columns; sums over the
+// rows are shuffles, and nothing is shared between warps (no barrier, so runs of rows and small batches
+// are as short as their loads).  CG neighbouring lanes read 16 CG consecutive bytes of a row: 64 (d = 128)
+// or 128.  Many bytes in flight matter most: at d = 128, 512 sequences of 32 heads, bf16 rows, 16 rows
+// a lane and 4 CTAs an SM take 324 us (6.69 TB/s, of a measured copy rate of 6.56), 3 CTAs 353 us, 8 rows
+// and 6 CTAs 370 us, 8 rows unbounded 439 us, and a ring of TMA copies through shared memory 352 us.
+// d = 64 at 2000 sequences 329 us (6.51 TB/s), d = 32 86 us (6.36 TB/s).
+template <int D>
+struct StepShape {
+  static constexpr int R = D == 128 ? 16 : 8, CG = 32 * R / D, warps = D / (4 * CG), per_sm = D == 128 ? 4 : 6;
+};
+
 template <typename T, typename TO, int D>
-__global__ void __launch_bounds__(kStepThreads, 6) kda_step_regs(StepArgs a) {
-  constexpr int R = 8, CG = 256 / D, SL = D / (4 * CG);  // rows per lane, column groups, warps per head
+__global__ void __launch_bounds__(kStepThreads, StepShape<D>::per_sm) kda_step_kernel(StepArgs a) {
+  constexpr int R = StepShape<D>::R, CG = StepShape<D>::CG, SL = StepShape<D>::warps;
   const int lane = threadIdx.x & 31, rg = lane / CG;
   const int64_t unit = (int64_t)blockIdx.x * (kStepThreads / 32) + (threadIdx.x >> 5);
   const int64_t bh = unit / SL;
@@ -198,184 +204,6 @@ __global__ void __launch_bounds__(kStepThreads, 6) kda_step_regs(StepArgs a) {
   float* dp = a.state + ((size_t)dst * a.H + h) * D * D + at;
 #pragma unroll
   for (int i = 0; i < R; ++i) store4(dp + (size_t)i * D, S[i]);
-}
-
-constexpr int kStepCols = 32, kStepPerSm = 4;
-
-template <int D>
-struct StepSmem {
-  static constexpr int stages = D == 128 ? 3 : D == 64 ? 6 : 8;
-  static constexpr uint32_t tile = D * kStepCols * 4;
-  static constexpr uint32_t vec = stages * tile, red = vec + 2 * D * 16, kq = red + 2 * 4 * 2 * kStepCols * 4;
-  static constexpr uint32_t bars = kq + 2 * 4 * 4, total = bars + 8 * stages + 128;  // + slack to align the tiles
-};
-
-// The same through shared memory, for large batches at d = 128: a unit of work is 32 columns of one
-// head's state, fetched and stored by TMA through a ring, so that the copies of the next units are in
-// flight while this one is computed (four CTAs an SM, 48 KB of states each).  Lane = column, warp = a
-// quarter of the rows (held in registers over a run's rows); the four partial sums of a column meet in
-// shared memory.  512 sequences of 32 heads: 352 us (6.16 TB/s; fp32 rows 339 us, 6.46 TB/s), the
-// kernel above 370 us (447 us).  At d = 64 a unit is 8 KB and its barriers cost more than they save
-// (569 against 409 us at 2000 sequences).
-template <typename T, typename TO, int D>
-__global__ void __launch_bounds__(kStepThreads, kStepPerSm)
-    kda_step_ring(const __grid_constant__ CUtensorMap tma_state, StepArgs a) {
-  using namespace tc;
-  using L = StepSmem<D>;
-  constexpr int R = D / 4, SL = D / kStepCols, NS = L::stages;  // rows per warp, units per head
-  extern __shared__ __align__(128) uint8_t ssm_raw[];
-  uint8_t* sm = ssm_raw + ((128u - (smem_u32(ssm_raw) & 127u)) & 127u);
-  float4* vec = reinterpret_cast<float4*>(sm + L::vec);  // [2][D]: e^g k, e^g q, e^g, k of a row
-  float* red = reinterpret_cast<float*>(sm + L::red);    // [2][warp][u, w][column]
-  float* skq = reinterpret_cast<float*>(sm + L::kq);     // [2][warp]
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::bars);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t units = (int64_t)a.rows.n_seqs * a.H * SL;
-  struct Unit {
-    int b, h, c0, src, dst, t0, t1;
-    bool ok;
-  };
-  auto unit_of = [&](int64_t u) {
-    Unit x{};
-    if (u >= units) return x;
-    x.c0 = (int)(u % SL) * kStepCols;
-    const int64_t bh = u / SL;
-    x.h = (int)(bh % a.H);
-    x.b = (int)(bh / a.H);
-    x.src = a.src[x.b];
-    x.dst = a.dst ? a.dst[x.b] : x.src;
-    x.t0 = a.rows.row_start ? a.rows.row_start[x.b] : x.b;
-    x.t1 = a.rows.row_start ? a.rows.row_start[x.b + 1] : x.b + 1;
-    x.ok = x.src >= 0;  // else a padding entry
-    if (x.ok && (x.src >= a.n_slots || x.dst < 0 || x.dst >= a.n_slots || x.t0 < 0 || x.t1 < x.t0 || x.t1 > a.rows.n_rows)) {
-      set_status(a.status, kStatusCheck);
-      x.ok = false;
-    }
-    return x;
-  };
-  auto issue = [&](int64_t u, int st) {  // thread 0: the state of unit u into stage st
-    const Unit x = unit_of(u);
-    if (!x.ok) {
-      mbar_arrive(&full[st]);
-      return;
-    }
-    mbar_arrive_expect_tx(&full[st], L::tile);
-    tma_load_2d(sm + st * L::tile, &tma_state, x.c0, (int)(((int64_t)x.src * a.H + x.h) * D), &full[st]);
-  };
-  // this thread's share of a token: row tid of q, k, g; column c0 + lane of v
-  float q = 0.f, k = 0.f, g = 0.f, v = 0.f, beta = 0.f;
-  auto load_row = [&](const Unit& x, int t) {
-    const size_t row = (size_t)t * a.H + x.h;
-    if (tid < D) {
-      q = to_f(((const T*)a.q)[row * D + tid]);
-      k = to_f(((const T*)a.k)[row * D + tid]);
-      g = to_f(((const T*)a.g)[row * D + tid]);
-    }
-    v = to_f(((const T*)a.v)[row * D + x.c0 + lane]);
-    beta = to_f(((const T*)a.beta)[row]);
-  };
-  if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    for (int i = 0; i < NS - 1; ++i) {
-      const int64_t u = blockIdx.x + (int64_t)i * gridDim.x;
-      if (u < units) issue(u, i);
-    }
-  }
-  __syncthreads();
-  Unit cur = unit_of(blockIdx.x);
-  if (cur.ok && cur.t0 < cur.t1) load_row(cur, cur.t0);
-  int st = 0, buf = 0;
-  uint32_t parity = 0;
-#pragma unroll 1
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const Unit nxt = unit_of(u + gridDim.x);
-    const bool more = nxt.ok && nxt.t0 < nxt.t1;
-    // the first unit of a sequence looks for another sequence that writes or reads the slot it writes
-    if (a.status && cur.ok && cur.h == 0 && cur.c0 == 0) {
-      bool clash = false;
-      for (int j = tid; j < a.rows.n_seqs; j += kStepThreads) {
-        const int sj = a.src[j];
-        if (j != cur.b && sj >= 0) clash |= sj == cur.dst || (a.dst && a.dst[j] == cur.dst);
-      }
-      if (clash) set_status(a.status, kStatusCheck);
-    }
-    const bool got = mbar_wait(&full[st], parity, 2000000000ull);
-    if (!got) set_status(a.status, 8);
-    if (cur.ok) {
-      float* tile = reinterpret_cast<float*>(sm + st * L::tile) + (warp * R) * kStepCols + lane;
-      float S[R];
-#pragma unroll
-      for (int i = 0; i < R; ++i) S[i] = tile[i * kStepCols];
-      if (cur.t0 == cur.t1 && more) load_row(nxt, nxt.t0);
-#pragma unroll 1
-      for (int t = cur.t0; t < cur.t1; ++t, buf ^= 1) {
-        float kq = 0.f;
-        if (tid < D) {
-          const float al = expf(g);
-          vec[buf * D + tid] = make_float4(al * k, al * q, al, k);
-          kq = k * q;
-        }
-#pragma unroll
-        for (int m = 16; m; m >>= 1) kq += __shfl_xor_sync(0xffffffffu, kq, m);
-        if (lane == 0) skq[buf * 4 + warp] = kq;
-        const float v_now = v, b_now = beta;
-        __syncthreads();
-        if (t + 1 < cur.t1)
-          load_row(cur, t + 1);
-        else if (more)
-          load_row(nxt, nxt.t0);
-        const float4* f = vec + buf * D + warp * R;
-        float p = 0.f, w = 0.f;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const float4 x = f[i];
-          p = fmaf(S[i], x.x, p);
-          w = fmaf(S[i], x.y, w);
-        }
-        float* rd = red + buf * 4 * 2 * kStepCols;
-        rd[(2 * warp) * kStepCols + lane] = p;
-        rd[(2 * warp + 1) * kStepCols + lane] = w;
-        __syncthreads();
-        p = w = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p += rd[(2 * i) * kStepCols + lane];
-          w += rd[(2 * i + 1) * kStepCols + lane];
-        }
-        const float delta = b_now * (v_now - p);
-        if (warp == 0) {
-          kq = skq[buf * 4] + skq[buf * 4 + 1] + skq[buf * 4 + 2] + skq[buf * 4 + 3];
-          ((TO*)a.o)[((size_t)t * a.H + cur.h) * D + cur.c0 + lane] = from_f<TO>(fmaf(kq, delta, w));
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const float4 x = f[i];
-          S[i] = fmaf(S[i], x.z, x.w * delta);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i) tile[i * kStepCols] = S[i];
-      fence_async_smem();
-      if (__syncthreads_and(got) && tid == 0)
-        tma_store_2d(sm + st * L::tile, &tma_state, cur.c0, (int)(((int64_t)cur.dst * a.H + cur.h) * D));
-    } else if (more) {
-      load_row(nxt, nxt.t0);
-    }
-    if (tid == 0) {
-      bulk_commit();
-      // the stage before this one is refilled once its store (all but the newest) has read it
-      bulk_wait_read_1();
-      const int64_t ahead = u + (int64_t)(NS - 1) * gridDim.x;
-      if (ahead < units) issue(ahead, st == 0 ? NS - 1 : st - 1);
-    }
-    cur = nxt;
-    if (++st == NS) {
-      st = 0;
-      parity ^= 1;
-    }
-  }
-  if (tid == 0) bulk_wait_all();
 }
 
 // ------------------------------------------------------------------------------------ cache append

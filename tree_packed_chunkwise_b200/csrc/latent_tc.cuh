@@ -181,6 +181,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// 32 fp32 accumulator values (as tmem_ld32_nowait gives them) rounded to bf16 at p (16-byte aligned)
+__device__ __forceinline__ void round_to_smem(const uint32_t (&r)[32], uint8_t* p) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    uint32_t e[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e[j] = pack_bf16(__uint_as_float(r[i + 2 * j]), __uint_as_float(r[i + 2 * j + 1]));
+    *reinterpret_cast<uint4*>(p + 2 * i) = make_uint4(e[0], e[1], e[2], e[3]);
+  }
+}
+
 // Persistent: the token tiles of all (sequence, column tile) units are one list, cut into equal
 // shares, one CTA each, so ragged lengths balance and one long context uses every SM.  The shares are
 // found on the device from kv_len (no host copy, graphs replay with new lengths).  A unit that is cut
@@ -750,57 +761,189 @@ __global__ void __launch_bounds__(kLatCombThreads) latent_combine_kernel(LatAttn
 }
 
 // ------------------------------------------------------------------------------------ per-head products
-// Y[t][h][n] = sum_k X[t][h][k] B_h[k][n] of the absorbed form, one CTA per (128 rows, head, BN outputs):
-//   kAbsorb: X = q_nope (K = 128), B_h = W_k[h] as it is stored ([k][n], MN-major), 512 outputs;
-//   kExpand: X = o (K = 512), B_h = W_v[h]^T (stored [n][k], K-major), 128 outputs.
-// Bound by reading X and writing Y (K is short); the weights and the re-read rows come from L2.  Two or
-// three CTAs share an SM and hide one another's latency, so a CTA does one tile: warp 0 loads K steps
-// of 64 by TMA, warp 1 issues M = 128 MMAs, warps 2-5 round the accumulator to bf16 and write whole
-// 256-byte row pieces through shared memory.
-enum : int { kAbsorb = 0, kExpand = 1 };
+// The absorbed queries qa[t][h][l] = sum_i q[t][h][i] W_k[h][i][l] (K = 128, 512 outputs) and their rotary
+// part.  Bound by writing qa (the weights and q are read from L2 after their first use).  A CTA takes 128
+// rows of a head and `blocks` of the four 128-wide output blocks: the rows stay in shared memory, the
+// weights (stored [i][l], MN-major) follow in steps of 64 i, and two accumulators alternate, so that
+// rounding and writing a block overlaps the next block's loads and MMAs.  Two CTAs share an SM.  Four
+// blocks a CTA once that fills every SM twice, two once it fills them (16 heads, us with 1 / 2 / 4 blocks:
+// 96 rows 4.3 / 5.1 / 7.4, 640 rows 8.2 / 7.7 / 8.4, 1300 rows 12.1 / 10.8 / 11.9, 4096 rows 37.8 / 28.5 /
+// 26.6, that is 3.86 TB/s).  The rotary parts of all rows are spread over the CTAs' writing warps.
 constexpr int kHeadTcThreads = 192;
 
-template <int KIND, int BN>
-struct HeadSmem {
-  static constexpr int K = KIND == kAbsorb ? kLatHead : kLatDim, steps = K / 64, N = KIND == kAbsorb ? kLatDim : kLatHead;
-  static constexpr int stages = KIND == kAbsorb ? 2 : 3;
-  static constexpr uint32_t a = 128 * 128, stage = a + BN * 128, out_ld = BN * 2 + 16;
-  static constexpr uint32_t total = stages * stage + 1024;  // + slack to align the stages to 1024 bytes
+struct AbsorbSmem {
+  static constexpr int w_slots = 3;
+  static constexpr uint32_t x = 2 * 128 * 128, w = 64 * 256, out_ld = 64 * 2 + 16;
+  static constexpr uint32_t out = x + w_slots * w, total = out + 128 * out_ld + 1024;  // + slack to align the tiles
+};
+
+struct AbsorbArgs {
+  DecodeRows rows;
+  int H;
+  const __nv_bfloat16* q;
+  int64_t ld_q;
+  __nv_bfloat16* qa;
+  int* status;
+  int blocks;  // output blocks per CTA: 1, 2 or 4
+};
+
+__global__ void __launch_bounds__(kHeadTcThreads)
+    latent_absorb_tc(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, AbsorbArgs a) {
+  using namespace tc;
+  using L = AbsorbSmem;
+  extern __shared__ __align__(1024) uint8_t hsm_raw[];
+  uint8_t* sm = hsm_raw + ((1024u - (smem_u32(hsm_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) uint64_t x_full[2], w_full[L::w_slots], w_empty[L::w_slots], acc_full[2], acc_empty[2];
+  __shared__ uint32_t tslot;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  // tile order: output blocks, then heads, fastest, so that CTAs in flight read the same rows
+  int tile = (int)blockIdx.x;
+  const int per_head = kLatDim / 128 / a.blocks, nb0 = tile % per_head * a.blocks;
+  tile /= per_head;
+  const int h = tile % a.H, t0 = tile / a.H * 128;
+  if (tid == 0) {
+    prefetch_tensor_map(&tma_x);
+    prefetch_tensor_map(&tma_w);
+    for (int i = 0; i < L::w_slots; ++i) {
+      mbar_init(&w_full[i], 1);
+      mbar_init(&w_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&x_full[i], 1);
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (w == 1) tmem_alloc(&tslot, 256);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tb = tslot;
+  // every wait is bounded; a role whose wait ran out records it and stops
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_wait(bar, parity, 2000000000ull)) return true;
+    set_status(a.status, 8);
+    return false;
+  };
+  const int items = 2 * a.blocks;  // (block, half of K)
+  if (w == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (; issued < items; ++issued) {
+        const int st = issued % L::w_slots, kc = issued & 1, n0 = (nb0 + (issued >> 1)) * 128;
+        if (issued >= L::w_slots && !wait(&w_empty[st], (issued / L::w_slots - 1) & 1)) break;
+        if (issued < 2) {
+          mbar_arrive_expect_tx(&x_full[kc], 128 * 128);
+          tma_load_3d(sm + kc * 128 * 128, &tma_x, 64 * kc, h, t0, &x_full[kc]);
+        }
+        uint8_t* ws = sm + L::x + st * L::w;
+        mbar_arrive_expect_tx(&w_full[st], L::w);
+        tma_load_2d(ws, &tma_w, n0, h * kLatHead + 64 * kc, &w_full[st]);
+        tma_load_2d(ws + L::w / 2, &tma_w, n0 + 64, h * kLatHead + 64 * kc, &w_full[st]);
+      }
+      if (issued < items)  // copies in flight land before the CTA ends
+        for (int i = max(0, issued - L::w_slots); i < issued; ++i) mbar_wait(&w_full[i % L::w_slots], (i / L::w_slots) & 1, 100000000ull);
+    }
+  } else if (w == 1) {
+    const uint32_t lead = elect_one();
+    constexpr uint32_t id = idesc_bf16(128, 128, false, true);
+    bool ok = true;
+    int st = 0, parity = 0;
+    for (int nb = 0; nb < a.blocks && ok; ++nb) {
+      const uint32_t acc = tb + (nb & 1) * 128;
+      if (nb >= 2) ok = __all_sync(0xffffffffu, wait(&acc_empty[nb & 1], ((nb >> 1) - 1) & 1));
+#pragma unroll
+      for (int kc = 0; kc < 2; ++kc) {
+        ok = ok && __all_sync(0xffffffffu, wait(&x_full[kc], 0) && wait(&w_full[st], parity));
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t xs = smem_u32(sm) + kc * 128 * 128, ws = smem_u32(sm) + L::x + st * L::w;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16_if(lead, acc, sw_desc_k(xs, 128, ks), sw_desc_mn(ws, 64, ks), id, kc || ks ? 1u : 0u);
+        commit_if(lead, &w_empty[st]);
+        if (++st == L::w_slots) {
+          st = 0;
+          parity ^= 1;
+        }
+      }
+      if (ok) commit_if(lead, &acc_full[nb & 1]);
+    }
+    // the last MMAs are complete before TMEM is freed
+    for (int nb = max(0, a.blocks - 2); nb < a.blocks && ok; ++nb) wait(&acc_full[nb & 1], (nb >> 1) & 1);
+    __syncwarp();
+  } else {
+    const int sp = w & 3;
+    int first = 0, last = a.rows.n_rows;  // rows that belong to a sequence
+    if (a.rows.row_start) {
+      first = a.rows.row_start[0];
+      last = min(last, a.rows.row_start[a.rows.n_seqs]);
+    }
+    // this CTA's share of the rotary parts, while the first copies and MMAs run
+    const int64_t r1 = (int64_t)a.rows.n_rows * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t t = (int64_t)a.rows.n_rows * blockIdx.x / gridDim.x + w - 2; t < r1; t += 4)
+      absorb_rope_row(a.rows, a.H, a.q, a.ld_q, a.qa, (int)t);
+    uint8_t* out = sm + L::out + 32 * sp * L::out_ld;  // this warp's rows
+    for (int nb = 0; nb < a.blocks; ++nb) {
+      if (!__all_sync(0xffffffffu, wait(&acc_full[nb & 1], (nb >> 1) & 1))) break;
+      fence_after_sync();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          uint32_t r[32];
+          tmem_ld32_nowait(tb + ((uint32_t)(32 * sp) << 16) + (nb & 1) * 128 + half * 64 + c0, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+          round_to_smem(r, out + lane * L::out_ld + c0 * 2);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = lane >> 3; i < 32; i += 4) {
+          const int t = t0 + 32 * sp + i;
+          if (t >= first && t < last)
+            *reinterpret_cast<uint4*>(a.qa + ((size_t)t * a.H + h) * kLatWidth + (nb0 + nb) * 128 + half * 64 + (lane & 7) * 8) =
+                *reinterpret_cast<const uint4*>(out + i * L::out_ld + (lane & 7) * 16);
+        }
+        __syncwarp();
+      }
+      fence_before_sync();
+      if (lane == 0) mbar_arrive(&acc_empty[nb & 1]);
+    }
+  }
+  __syncthreads();
+  if (w == 1) tmem_dealloc(tb, 256);
+}
+
+// The head outputs out[t][h][i] = sum_l W_v[h][i][l] o[t][h][l] (K = 512, 128 outputs), one CTA per 128 rows
+// and head.  Bound by reading o.  K steps of 64 through three stages (both operands K-major), M = 128
+// MMAs, the outputs written in whole 256-byte row pieces through the stages' memory.  Two CTAs share an SM
+// and hide one another's epilogue (2047 rows of 32 heads: 14.8 us, 5.94 TB/s).
+struct ExpandSmem {
+  static constexpr int stages = 3, steps = kLatDim / 64;
+  static constexpr uint32_t half = 128 * 128, stage = 2 * half, out_ld = kLatHead * 2 + 16;
+  static constexpr uint32_t total = stages * stage + 1024;  // + slack to align the stages
   static_assert(128 * out_ld <= stages * stage, "the output tile takes the stages' place");
 };
 
-struct HeadArgs {
-  DecodeRows rows;  // kAbsorb: positions, and the rows that belong to a sequence
+struct ExpandArgs {
   int H, n_rows;
-  const __nv_bfloat16* q;  // kAbsorb: rotary part
-  int64_t ld_q;
-  __nv_bfloat16* y;
+  __nv_bfloat16* out;
   int* status;
-  int rope_ctas;  // leading CTAs that turn the rotary parts (kAbsorb)
 };
 
-template <int KIND, int BN>
 __global__ void __launch_bounds__(kHeadTcThreads)
-    latent_head_tc(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, HeadArgs a) {
+    latent_expand_tc(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, ExpandArgs a) {
   using namespace tc;
-  using L = HeadSmem<KIND, BN>;
+  using L = ExpandSmem;
   extern __shared__ __align__(1024) uint8_t hsm_raw[];
   uint8_t* sm = hsm_raw + ((1024u - (smem_u32(hsm_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t full[L::stages], empty[L::stages], acc_full;
   __shared__ uint32_t tslot;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  if constexpr (KIND == kAbsorb) {
-    if ((int)blockIdx.x < a.rope_ctas) {
-      const int64_t t = (int64_t)blockIdx.x * (kHeadTcThreads / 32) + w;
-      if (t < a.n_rows) absorb_rope_row(a.rows, a.H, a.q, a.ld_q, a.y, (int)t);
-      return;
-    }
-  }
-  // tile order: output blocks, then heads, fastest, so that CTAs in flight read the same rows
-  int tile = (int)blockIdx.x - a.rope_ctas;
-  const int n0 = tile % (L::N / BN) * BN;
-  tile /= L::N / BN;
-  const int h = tile % a.H, t0 = tile / a.H * 128;
+  const int h = (int)(blockIdx.x % a.H), t0 = (int)(blockIdx.x / a.H) * 128;
   if (tid == 0) {
     prefetch_tensor_map(&tma_x);
     prefetch_tensor_map(&tma_w);
@@ -811,12 +954,12 @@ __global__ void __launch_bounds__(kHeadTcThreads)
     mbar_init(&acc_full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (w == 1) tmem_alloc(&tslot, BN);
+  if (w == 1) tmem_alloc(&tslot, 128);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tb = tslot;
-  // every wait is bounded; a role whose wait ran out records it and goes on without the data
+  // every wait is bounded; a role whose wait ran out records it and stops
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (mbar_wait(bar, parity, 2000000000ull)) return true;
     set_status(a.status, 8);
@@ -831,19 +974,14 @@ __global__ void __launch_bounds__(kHeadTcThreads)
         uint8_t* xs = sm + st * L::stage;
         mbar_arrive_expect_tx(&full[st], L::stage);
         tma_load_3d(xs, &tma_x, k0, h, t0, &full[st]);
-        if constexpr (KIND == kAbsorb) {
-          for (int j = 0; j < BN / 64; ++j)
-            tma_load_2d(xs + L::a + j * 64 * 128, &tma_w, n0 + 64 * j, h * kLatHead + k0, &full[st]);
-        } else {
-          tma_load_2d(xs + L::a, &tma_w, k0, (a.H + h) * kLatHead + n0, &full[st]);
-        }
+        tma_load_2d(xs + L::half, &tma_w, k0, (a.H + h) * kLatHead, &full[st]);
       }
       if (issued < L::steps)  // copies in flight land before the CTA ends
         for (int i = max(0, issued - L::stages); i < issued; ++i) mbar_wait(&full[i % L::stages], (i / L::stages) & 1, 100000000ull);
     }
   } else if (w == 1) {
     const uint32_t lead = elect_one();
-    constexpr uint32_t id = idesc_bf16(128, BN, false, KIND == kAbsorb);
+    constexpr uint32_t id = idesc_bf16(128, 128, false, false);
     bool ok = true;
 #pragma unroll
     for (int i = 0; i < L::steps; ++i) {
@@ -853,50 +991,42 @@ __global__ void __launch_bounds__(kHeadTcThreads)
       fence_after_sync();
       const uint32_t xs = smem_u32(sm) + st * L::stage;
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        mma_bf16_if(lead, tb, sw_desc_k(xs, 128, ks),
-                    KIND == kAbsorb ? sw_desc_mn(xs + L::a, 64, ks) : sw_desc_k(xs + L::a, BN, ks), id, i || ks ? 1u : 0u);
+      for (int ks = 0; ks < 4; ++ks) mma_bf16_if(lead, tb, sw_desc_k(xs, 128, ks), sw_desc_k(xs + L::half, 128, ks), id, i || ks ? 1u : 0u);
       commit_if(lead, &empty[st]);
     }
-    commit_if(lead, &acc_full);
-    wait(&acc_full, 0);
+    // also after a wait that ran out: the MMAs issued so far are complete before TMEM is freed, but then
+    // the epilogue must not take the accumulator for whole
+    if (ok) commit_if(lead, &acc_full);
+    if (ok) wait(&acc_full, 0);
     __syncwarp();
   } else {
     const int sp = w & 3;
     const bool got = __all_sync(0xffffffffu, wait(&acc_full, 0));
     fence_after_sync();
-    int first = 0, last = a.n_rows;  // rows that belong to a sequence
-    if (KIND == kAbsorb && a.rows.row_start) {
-      first = a.rows.row_start[0];
-      last = min(last, a.rows.row_start[a.rows.n_seqs]);
-    }
     uint8_t* out = sm + 32 * sp * L::out_ld;  // this warp's rows; every copy has landed and been read
+    if (got) {
 #pragma unroll
-    for (int c0 = 0; c0 < BN; c0 += 32) {
-      uint32_t r[32];
-      tmem_ld32_nowait(tb + ((uint32_t)(32 * sp) << 16) + c0, r);
-      tmem_wait_ld();
+      for (int c0 = 0; c0 < kLatHead; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32_nowait(tb + ((uint32_t)(32 * sp) << 16) + c0, r);
+        tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
-#pragma unroll
-      for (int i = 0; i < 32; i += 8)
-        *reinterpret_cast<uint4*>(out + lane * L::out_ld + (c0 + i) * 2) = make_uint4(
-            pack_bf16(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), pack_bf16(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])),
-            pack_bf16(__uint_as_float(r[i + 4]), __uint_as_float(r[i + 5])), pack_bf16(__uint_as_float(r[i + 6]), __uint_as_float(r[i + 7])));
-    }
-    __syncwarp();
-    constexpr int lanes = BN / 8, at_once = 32 / lanes, width = KIND == kAbsorb ? kLatWidth : kLatHead;
+        for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+        round_to_smem(r, out + lane * L::out_ld + c0 * 2);
+      }
+      __syncwarp();
 #pragma unroll 4
-    for (int i = lane / lanes; i < 32; i += at_once) {
-      const int t = t0 + 32 * sp + i;
-      if (got && t >= first && t < last)
-        *reinterpret_cast<uint4*>(a.y + ((size_t)t * a.H + h) * width + n0 + lane % lanes * 8) =
-            *reinterpret_cast<const uint4*>(out + i * L::out_ld + lane % lanes * 16);
+      for (int i = lane >> 4; i < 32; i += 2) {
+        const int t = t0 + 32 * sp + i;
+        if (t < a.n_rows)
+          *reinterpret_cast<uint4*>(a.out + ((size_t)t * a.H + h) * kLatHead + (lane & 15) * 8) =
+              *reinterpret_cast<const uint4*>(out + i * L::out_ld + (lane & 15) * 16);
+      }
     }
     fence_before_sync();
   }
   __syncthreads();
-  if (w == 1) tmem_dealloc(tb, BN);
+  if (w == 1) tmem_dealloc(tb, 128);
 }
 
 }  // namespace tpc

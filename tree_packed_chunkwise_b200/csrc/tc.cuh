@@ -194,8 +194,6 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // waits until this thread's committed bulk stores have finished reading shared memory
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-// the same for all but the newest committed group
-__device__ __forceinline__ void bulk_wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 // waits until this thread's committed bulk stores are complete (visible in global memory)
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
@@ -222,14 +220,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
           smem_u32(dst)),
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
-}
-
-// Tiled TMA store (2-D tensor map) of this CTA's shared memory (bulk async-group of the issuing thread);
-// the innermost coordinate x a multiple of 16 bytes' worth of elements, coordinates not negative.
-__device__ __forceinline__ void tma_store_2d(const void* src, const void* tmap, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(tmap), "r"(x), "r"(y),
-               "r"(smem_u32(src))
-               : "memory");
 }
 
 // Descriptors of 128-byte-swizzled bf16 operand tiles stored as 64-column TMA boxes of `rows` rows
