@@ -150,3 +150,14 @@ def test_oracle_step_equals_tree_recurrence():
     q, k, v, g, b = (x[idx].astype(np.float64) for x in inputs)
     o, new, _, _ = od.kda_step(np.zeros((1, 2, 32, 32)), [0], [0], q, k, v, g, b, np.array([0, len(idx)]))
     assert np.abs(o - o_ref[idx]).max() < 1e-12 and np.abs(new[0] - fin_ref[1]).max() < 1e-12
+
+
+def test_packed_structs_have_the_c_layout(tpc):
+    """The wrappers pack the C structs as bytes: the same fields as the ctypes classes, at the same offsets."""
+    def same(cls, packed, *values):
+        want = cls(*values)
+        assert packed == bytes(want), cls
+    same(tpc.Rows, tpc._pack_rows(3, 2, A, 2 * A), 3, 2, A, 2 * A)
+    same(tpc.LatentCache, tpc._pack_cache(A, 5, 64, 2 * A, 7), A, 5, 64, 2 * A, 7)
+    same(tpc.KdaStepIO, tpc._pack_step(*range(1, 7), 9, 10, 0, 11), *range(1, 7), 9, 10, 0, 11)
+    same(tpc.KdaShape, tpc._pack_shape(2, 128, 128, True, False), 2, 128, 128, 1, 0)

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -164,12 +165,13 @@ SIGNATURES = {
     "tpc_group_backward": (ctypes.c_int, [_V, _P(GroupShape), _P(GroupWeights), _V, _V, _V, _V, _P(GroupGrads), _V,
                                           ctypes.c_size_t, _V]),
     "tpc_group_status": (ctypes.c_int, [_V, _P(GroupShape), _V, _V]),
-    "tpc_kda_step": (ctypes.c_int, [_P(KdaShape), _P(Rows), _P(KdaStepIO), _V, _V]),
-    "tpc_latent_append": (ctypes.c_int, [_P(LatentCache), _P(Rows), _V, ctypes.c_int64, _V, ctypes.c_int64,
+    # their structs are passed as _V: packed bytes (_pack_*) or a reference to the class
+    "tpc_kda_step": (ctypes.c_int, [_V, _V, _V, _V, _V]),
+    "tpc_latent_append": (ctypes.c_int, [_V, _V, _V, ctypes.c_int64, _V, ctypes.c_int64,
                                          ctypes.c_int32, _V, _V]),
-    "tpc_latent_absorb": (ctypes.c_int, [_P(Rows), ctypes.c_int32, _V, ctypes.c_int64, _V, _V, _V, _V]),
+    "tpc_latent_absorb": (ctypes.c_int, [_V, ctypes.c_int32, _V, ctypes.c_int64, _V, _V, _V, _V]),
     "tpc_latent_attn_scratch_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
-    "tpc_latent_attn": (ctypes.c_int, [_P(LatentCache), _P(Rows), ctypes.c_int32, ctypes.c_float, _V, _V, _V, _V,
+    "tpc_latent_attn": (ctypes.c_int, [_V, _V, ctypes.c_int32, ctypes.c_float, _V, _V, _V, _V,
                                        ctypes.c_size_t, _V, _V]),
     "tpc_latent_expand": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _V, _V, _V, _V, _V]),
     "tpc_profile_enable": (None, [ctypes.c_int]),
@@ -817,64 +819,101 @@ def tpc_group_status(plan: Plan, ws, n_kda: int = 3, stream=None) -> int:
 
 
 # ------------------------------------------------------------------------------------ token-by-token generation
+# A decoded token's kernels take a few microseconds, so these calls keep the host's share small: one
+# comparison chain per tensor, and the C structs packed as bytes (layouts as in include/tpc.h).
 LATENT_DIM, LATENT_ROPE, LATENT_HEAD, LATENT_WIDTH = 512, 64, 128, 576
+_pack_shape = struct.Struct("@5i").pack        # tpc_kda_shape
+_pack_rows = struct.Struct("@iiPP").pack       # tpc_rows
+_pack_step = struct.Struct("@6Pi3P").pack      # tpc_kda_step_io
+_pack_cache = struct.Struct("@PiiPi0P").pack   # tpc_latent_cache
 
 
-def _want(name, t, shape, dtypes, dev, contiguous=True):
-    """Raises TpcError (TPC_ERR_BAD_SHAPE) unless t has the shape, one of the dtypes and lives on dev."""
-    if tuple(t.shape) != shape:
-        raise TpcError(2, f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.dtype not in dtypes:
-        raise TpcError(2, f"{name} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if t.device != dev:
-        raise TpcError(2, f"{name} is on {t.device}, not on {dev}")
-    if contiguous and not t.is_contiguous():
-        raise TpcError(2, f"{name} is not contiguous")
+def _want(name, t, dtype, shape, dev):
+    """The address of t; raises TpcError (TPC_ERR_BAD_SHAPE) unless t is contiguous with the dtype and shape, on
+    device index dev."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise TpcError(2, f"{name} must be a contiguous {dtype} tensor {shape} on cuda:{dev}, got {t.dtype} "
+                      f"{tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+
+
+def _want_rows(name, t, dtype, shape, dev):
+    """As _want for a tensor whose rows (dimension 0) may lie further apart: (address, elements from row to row)."""
+    n, inner = t.shape[0] if t.dim() else 0, 1
+    ok = t.dtype is dtype and t.shape == shape and t.get_device() == dev
+    for d in range(len(shape) - 1, 0, -1):
+        ok = ok and (t.stride(d) == inner or t.shape[d] == 1 or n == 0)
+        inner *= shape[d]
+    if not ok:
+        raise TpcError(2, f"{name} must be a {dtype} tensor {shape} with contiguous rows on cuda:{dev}, got {t.dtype} "
+                          f"{tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+    return t.data_ptr(), t.stride(0) if n > 1 else inner  # the stride of a single row says nothing
 
 
 def _decode_device(t):
-    """t's device, which must be the current CUDA device."""
+    """t's device index, which must be the current CUDA device."""
     import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise TpcError(2, f"tensors are on {t.device}, not on the current CUDA device")
-    return t.device
+    return dev
 
 
-def _decode_rows(n_rows, row_start, kv_len, n_seqs, dev, status):
+def _decode_stream(stream, dev):
     import torch
-    i32 = (torch.int32,)
-    if row_start is None and n_rows != n_seqs:
-        raise TpcError(2, f"{n_rows} rows for {n_seqs} sequences need row_start")
-    if row_start is not None:
-        _want("row_start", row_start, (n_seqs + 1,), i32, dev)
-    if kv_len is not None:
-        _want("kv_len", kv_len, (n_seqs,), i32, dev)
-    if status is not None:
-        _want("status", status, tuple(status.shape), i32, dev)
-        if status.numel() < 1:
-            raise TpcError(2, "status needs one element")
-    return Rows(n_rows, n_seqs, None if row_start is None else row_start.data_ptr(),
-                None if kv_len is None else kv_len.data_ptr())
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _decode_rows(n_rows, row_start, kv_len, n_seqs, dev):
+    """The packed tpc_rows of a batch (kv_len: its address)."""
+    import torch
+    if row_start is None:
+        if n_rows != n_seqs:
+            raise TpcError(2, f"{n_rows} rows for {n_seqs} sequences need row_start")
+        return _pack_rows(n_rows, n_seqs, 0, kv_len)
+    return _pack_rows(n_rows, n_seqs, _want("row_start", row_start, torch.int32, (n_seqs + 1,), dev), kv_len)
+
+
+def _status(status, dev):
+    import torch
+    if status is None:
+        return None
+    if status.numel() < 1:
+        raise TpcError(2, "status needs one element")
+    return _want("status", status, torch.int32, status.shape, dev)
+
+
+def _out(name, t, dtype, shape, dev, stream):
+    """(tensor, address) of an output: t checked, or a new one.  New memory belongs to the call's stream, so that
+    it is reused in that stream's order."""
+    import torch
+    if t is not None:
+        return t, _want(name, t, dtype, shape, dev)
+    if stream is None:
+        t = torch.empty(shape, dtype=dtype, device="cuda")
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device="cuda")
+    return t, t.data_ptr()
 
 
 def _latent_cache(cache, block_table, n_seqs, dev):
     import torch
-    if cache.dim() != 3:
-        raise TpcError(2, f"cache must be [n_pages, page_size, {LATENT_WIDTH}], got {tuple(cache.shape)}")
-    _want("cache", cache, (cache.shape[0], cache.shape[1], LATENT_WIDTH), (torch.bfloat16,), dev)
-    if block_table.dim() != 2:
-        raise TpcError(2, f"block_table must be [n_seqs, max_pages], got {tuple(block_table.shape)}")
-    _want("block_table", block_table, (n_seqs, block_table.shape[1]), (torch.int32,), dev)
-    return LatentCache(cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(), block_table.shape[1])
+    if cache.dim() != 3 or block_table.dim() != 2:
+        raise TpcError(2, f"cache must be [n_pages, page_size, {LATENT_WIDTH}] and block_table [n_seqs, max_pages], got "
+                          f"{tuple(cache.shape)} and {tuple(block_table.shape)}")
+    n_pages, page, _ = cache.shape
+    max_pages = block_table.shape[1]
+    return _pack_cache(_want("cache", cache, torch.bfloat16, (n_pages, page, LATENT_WIDTH), dev), n_pages, page,
+                       _want("block_table", block_table, torch.int32, (n_seqs, max_pages), dev), max_pages)
 
 
-def _new(stream, *shape, dtype, dev):
-    """An uninitialised tensor of the call's stream: its memory is reused in that stream's order."""
+def _kv_len(kv_len, dev):
+    """(address, sequences) of the cached lengths."""
     import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+    if kv_len.dim() != 1:
+        raise TpcError(2, f"kv_len must be [n_seqs], got {tuple(kv_len.shape)}")
+    return _want("kv_len", kv_len, torch.int32, kv_len.shape, dev), kv_len.shape[0]
 
 
 def tpc_kda_step(state, src, q, k, v, g, beta, dst=None, row_start=None, out_dtype=None, o=None, status=None,
@@ -884,32 +923,26 @@ def tpc_kda_step(state, src, q, k, v, g, beta, dst=None, row_start=None, out_dty
     (default: in place); row_start: int32 [n_seqs + 1] rows of each sequence (default: one each)."""
     import torch
     dev = _decode_device(state)
-    if q.dim() != 3 or state.dim() != 4:
-        raise TpcError(2, f"q must be [n_rows, H, d] and state [n_slots, H, d, d], got {tuple(q.shape)} and {tuple(state.shape)}")
-    n, H, d = q.shape
-    out_dtype = out_dtype or (o.dtype if o is not None else q.dtype)
-    both, one = (torch.bfloat16, torch.float32), (q.dtype,)
-    _want("q", q, (n, H, d), both, dev)
-    for name, t in (("k", k), ("v", v), ("g", g)):
-        _want(name, t, (n, H, d), one, dev)
-    _want("beta", beta, (n, H), one, dev)
-    _want("state", state, (state.shape[0], H, d, d), (torch.float32,), dev)
-    n_seqs = src.shape[0] if src.dim() == 1 else -1
-    _want("src", src, (n_seqs,), (torch.int32,), dev)
-    if dst is not None:
-        _want("dst", dst, (n_seqs,), (torch.int32,), dev)
-    rows = _decode_rows(n, row_start, None, n_seqs, dev, status)
-    if o is None:
-        o = _new(stream, n, H, d, dtype=out_dtype, dev=dev)
-    else:
-        _want("o", o, (n, H, d), (out_dtype,), dev)
-    if out_dtype not in both:
-        raise TpcError(2, f"out_dtype {out_dtype} is neither bf16 nor fp32")
-    shape = kda_shape(H, d, _dtype_code(q), TPC_BF16 if out_dtype == torch.bfloat16 else TPC_F32)
-    io = KdaStepIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(),
-                   state.shape[0], src.data_ptr(), None if dst is None else dst.data_ptr(), o.data_ptr())
-    _check(lib().tpc_kda_step(ctypes.byref(shape), ctypes.byref(rows), ctypes.byref(io), _ptr(status),
-                              _stream_ptr(stream)))
+    if q.dim() != 3 or state.dim() != 4 or src.dim() != 1:
+        raise TpcError(2, f"q must be [n_rows, H, d], state [n_slots, H, d, d] and src [n_seqs], got {tuple(q.shape)}, "
+                          f"{tuple(state.shape)} and {tuple(src.shape)}")
+    rows = n, H, d = q.shape
+    n_slots, n_seqs, dt, i32 = state.shape[0], src.shape[0], q.dtype, torch.int32
+    if out_dtype is None:
+        out_dtype = dt if o is None else o.dtype
+    bf, f32 = torch.bfloat16, torch.float32
+    if (dt is not bf and dt is not f32) or (out_dtype is not bf and out_dtype is not f32):
+        raise TpcError(2, f"rows and outputs are bf16 or fp32, got {dt} and {out_dtype}")
+    p = [_want(name, t, dt, rows, dev) for name, t in (("q", q), ("k", k), ("v", v), ("g", g))]
+    p_beta, p_state = _want("beta", beta, dt, (n, H), dev), _want("state", state, f32, (n_slots, H, d, d), dev)
+    p_src = _want("src", src, i32, (n_seqs,), dev)
+    p_dst = 0 if dst is None else _want("dst", dst, i32, (n_seqs,), dev)
+    batch = _decode_rows(n, row_start, 0, n_seqs, dev)
+    status = _status(status, dev)
+    o, p_o = _out("o", o, out_dtype, rows, dev, stream)
+    _check(lib().tpc_kda_step(_pack_shape(H, d, d, dt is bf, out_dtype is bf), batch,
+                              _pack_step(*p, p_beta, p_state, n_slots, p_src, p_dst, p_o), status,
+                              _decode_stream(stream, dev)))
     return o
 
 
@@ -919,41 +952,34 @@ def tpc_latent_append(cache, block_table, kv_len, c, kr, row_start=None, status=
     512] and kr [n_rows, 64]: bf16 or fp32, rows may be slices of a wider tensor."""
     import torch
     dev = _decode_device(cache)
-    if kv_len.dim() != 1 or c.dim() != 2:
-        raise TpcError(2, f"kv_len must be [n_seqs] and c [n_rows, {LATENT_DIM}]")
+    p_kv, n_seqs = _kv_len(kv_len, dev)
+    lc = _latent_cache(cache, block_table, n_seqs, dev)
+    dt = c.dtype
+    if c.dim() != 2 or (dt is not torch.bfloat16 and dt is not torch.float32):
+        raise TpcError(2, f"c must be bf16 or fp32 [n_rows, {LATENT_DIM}], got {dt} {tuple(c.shape)}")
     n = c.shape[0]
-    lc = _latent_cache(cache, block_table, kv_len.shape[0], dev)
-    _want("c", c, (n, LATENT_DIM), (torch.bfloat16, torch.float32), dev, contiguous=False)
-    _want("kr", kr, (n, LATENT_ROPE), (c.dtype,), dev, contiguous=False)
-    if n and (c.stride(1) != 1 or kr.stride(1) != 1):
-        raise TpcError(2, "the rows of c and kr must be contiguous")
-    rows = _decode_rows(n, row_start, kv_len, kv_len.shape[0], dev, status)
-    ld = lambda t, w: t.stride(0) if n > 1 else w  # the stride of a single row says nothing
-    _check(lib().tpc_latent_append(ctypes.byref(lc), ctypes.byref(rows), _ptr(c), ld(c, LATENT_DIM), _ptr(kr),
-                                   ld(kr, LATENT_ROPE), _dtype_code(c), _ptr(status), _stream_ptr(stream)))
+    p_c, ld_c = _want_rows("c", c, dt, (n, LATENT_DIM), dev)
+    p_kr, ld_kr = _want_rows("kr", kr, dt, (n, LATENT_ROPE), dev)
+    batch = _decode_rows(n, row_start, p_kv, n_seqs, dev)
+    _check(lib().tpc_latent_append(lc, batch, p_c, ld_c, p_kr, ld_kr, dt is torch.bfloat16, _status(status, dev),
+                                   _decode_stream(stream, dev)))
 
 
 def tpc_latent_absorb(q, w_b, kv_len, row_start=None, qa=None, status=None, stream=None):
     """Absorbed queries qa [n_rows, H, 576] (bf16) of q [n_rows, H, 192] (bf16; the rows may be slices of a wider
     tensor) and the group's w_b [2 * 128 * H, 512], the rotary part turned at the rows' positions (include/tpc.h)."""
     import torch
-    dev = _decode_device(q)
-    bf = (torch.bfloat16,)
-    if q.dim() != 3 or kv_len.dim() != 1:
-        raise TpcError(2, f"q must be [n_rows, H, {LATENT_HEAD + LATENT_ROPE}] and kv_len [n_seqs]")
+    dev, bf = _decode_device(q), torch.bfloat16
+    p_kv, n_seqs = _kv_len(kv_len, dev)
+    if q.dim() != 3:
+        raise TpcError(2, f"q must be [n_rows, H, {LATENT_HEAD + LATENT_ROPE}], got {tuple(q.shape)}")
     n, H, _ = q.shape
-    qk = LATENT_HEAD + LATENT_ROPE
-    _want("q", q, (n, H, qk), bf, dev, contiguous=False)
-    if n and (q.stride(2) != 1 or (H > 1 and q.stride(1) != qk)):
-        raise TpcError(2, "the rows of q must be contiguous")
-    _want("w_b", w_b, (2 * LATENT_HEAD * H, LATENT_DIM), bf, dev)
-    rows = _decode_rows(n, row_start, kv_len, kv_len.shape[0], dev, status)
-    if qa is None:
-        qa = _new(stream, n, H, LATENT_WIDTH, dtype=torch.bfloat16, dev=dev)
-    else:
-        _want("qa", qa, (n, H, LATENT_WIDTH), bf, dev)
-    _check(lib().tpc_latent_absorb(ctypes.byref(rows), H, _ptr(q), q.stride(0) if n > 1 else H * qk, _ptr(w_b),
-                                   _ptr(qa), _ptr(status), _stream_ptr(stream)))
+    p_q, ld_q = _want_rows("q", q, bf, (n, H, LATENT_HEAD + LATENT_ROPE), dev)
+    p_w = _want("w_b", w_b, bf, (2 * LATENT_HEAD * H, LATENT_DIM), dev)
+    batch = _decode_rows(n, row_start, p_kv, n_seqs, dev)
+    status = _status(status, dev)
+    qa, p_qa = _out("qa", qa, bf, (n, H, LATENT_WIDTH), dev, stream)
+    _check(lib().tpc_latent_absorb(batch, H, p_q, ld_q, p_w, p_qa, status, _decode_stream(stream, dev)))
     return qa
 
 
@@ -968,46 +994,33 @@ def tpc_latent_attn(qa, cache, block_table, kv_len, scale, row_start=None, o=Non
     """Absorbed latent attention of the new rows over the paged cache (include/tpc.h); returns (o [n_rows, H, 512]
     bf16, lse [n_rows, H] fp32).  qa: bf16 [n_rows, H, 576] of tpc_latent_absorb."""
     import torch
-    dev = _decode_device(qa)
-    bf = (torch.bfloat16,)
-    if qa.dim() != 3 or kv_len.dim() != 1:
-        raise TpcError(2, f"qa must be [n_rows, H, {LATENT_WIDTH}] and kv_len [n_seqs]")
+    dev, bf = _decode_device(qa), torch.bfloat16
+    p_kv, n_seqs = _kv_len(kv_len, dev)
+    if qa.dim() != 3:
+        raise TpcError(2, f"qa must be [n_rows, H, {LATENT_WIDTH}], got {tuple(qa.shape)}")
     n, H, _ = qa.shape
-    _want("qa", qa, (n, H, LATENT_WIDTH), bf, dev)
-    lc = _latent_cache(cache, block_table, kv_len.shape[0], dev)
-    rows = _decode_rows(n, row_start, kv_len, kv_len.shape[0], dev, status)
-    if o is None:
-        o = _new(stream, n, H, LATENT_DIM, dtype=torch.bfloat16, dev=dev)
-    else:
-        _want("o", o, (n, H, LATENT_DIM), bf, dev)
-    if lse is None:
-        lse = _new(stream, n, H, dtype=torch.float32, dev=dev)
-    else:
-        _want("lse", lse, (n, H), (torch.float32,), dev)
-    if scratch is None:
-        scratch = _new(stream, int(lib().tpc_latent_attn_scratch_bytes(H)), dtype=torch.uint8, dev=dev)
-    else:
-        _want("scratch", scratch, tuple(scratch.shape), (torch.uint8,), dev)
-    _check(lib().tpc_latent_attn(ctypes.byref(lc), ctypes.byref(rows), H, float(scale), _ptr(qa), _ptr(o), _ptr(lse),
-                                 _ptr(scratch), scratch.numel(), _ptr(status), _stream_ptr(stream)))
+    p_qa = _want("qa", qa, bf, (n, H, LATENT_WIDTH), dev)
+    lc = _latent_cache(cache, block_table, n_seqs, dev)
+    batch = _decode_rows(n, row_start, p_kv, n_seqs, dev)
+    status = _status(status, dev)
+    need = int(lib().tpc_latent_attn_scratch_bytes(H)) if scratch is None else scratch.numel()
+    scratch, p_scratch = _out("scratch", scratch, torch.uint8, (need,), dev, stream)
+    o, p_o = _out("o", o, bf, (n, H, LATENT_DIM), dev, stream)
+    lse, p_lse = _out("lse", lse, torch.float32, (n, H), dev, stream)
+    _check(lib().tpc_latent_attn(lc, batch, H, scale, p_qa, p_o, p_lse, p_scratch, need, status,
+                                 _decode_stream(stream, dev)))
     return o, lse
 
 
 def tpc_latent_expand(o, w_b, out=None, status=None, stream=None):
     """Head outputs [n_rows, H, 128] (bf16) of the attention's o [n_rows, H, 512] through w_b's value rows."""
     import torch
-    dev = _decode_device(o)
-    bf = (torch.bfloat16,)
+    dev, bf = _decode_device(o), torch.bfloat16
     if o.dim() != 3:
-        raise TpcError(2, f"o must be [n_rows, H, {LATENT_DIM}]")
+        raise TpcError(2, f"o must be [n_rows, H, {LATENT_DIM}], got {tuple(o.shape)}")
     n, H, _ = o.shape
-    _want("o", o, (n, H, LATENT_DIM), bf, dev)
-    _want("w_b", w_b, (2 * LATENT_HEAD * H, LATENT_DIM), bf, dev)
-    if status is not None:
-        _want("status", status, tuple(status.shape), (torch.int32,), dev)
-    if out is None:
-        out = _new(stream, n, H, LATENT_HEAD, dtype=torch.bfloat16, dev=dev)
-    else:
-        _want("out", out, (n, H, LATENT_HEAD), bf, dev)
-    _check(lib().tpc_latent_expand(n, H, _ptr(o), _ptr(w_b), _ptr(out), _ptr(status), _stream_ptr(stream)))
+    p_x, p_w = _want("o", o, bf, (n, H, LATENT_DIM), dev), _want("w_b", w_b, bf, (2 * LATENT_HEAD * H, LATENT_DIM), dev)
+    status = _status(status, dev)
+    out, p_out = _out("out", out, bf, (n, H, LATENT_HEAD), dev, stream)
+    _check(lib().tpc_latent_expand(n, H, p_x, p_w, p_out, status, _decode_stream(stream, dev)))
     return out
