@@ -8,6 +8,7 @@ without the built library or a CUDA device the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -828,6 +829,18 @@ _pack_step = struct.Struct("@6Pi3P").pack      # tpc_kda_step_io
 _pack_cache = struct.Struct("@PiiPi0P").pack   # tpc_latent_cache
 
 
+_torch_module = None
+
+
+def _torch():
+    """torch, imported on the first use (the planner needs none)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _want(name, t, dtype, shape, dev):
     """The address of t; raises TpcError (TPC_ERR_BAD_SHAPE) unless t is contiguous with the dtype and shape, on
     device index dev."""
@@ -852,53 +865,48 @@ def _want_rows(name, t, dtype, shape, dev):
 
 def _decode_device(t):
     """t's device index, which must be the current CUDA device."""
-    import torch
     dev = t.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
+    if dev < 0 or dev != _torch()._C._cuda_getDevice():
         raise TpcError(2, f"tensors are on {t.device}, not on the current CUDA device")
     return dev
 
 
 def _decode_stream(stream, dev):
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _torch_module._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _decode_rows(n_rows, row_start, kv_len, n_seqs, dev):
     """The packed tpc_rows of a batch (kv_len: its address)."""
-    import torch
     if row_start is None:
         if n_rows != n_seqs:
             raise TpcError(2, f"{n_rows} rows for {n_seqs} sequences need row_start")
         return _pack_rows(n_rows, n_seqs, 0, kv_len)
-    return _pack_rows(n_rows, n_seqs, _want("row_start", row_start, torch.int32, (n_seqs + 1,), dev), kv_len)
+    return _pack_rows(n_rows, n_seqs, _want("row_start", row_start, _torch_module.int32, (n_seqs + 1,), dev), kv_len)
 
 
 def _status(status, dev):
-    import torch
     if status is None:
         return None
     if status.numel() < 1:
         raise TpcError(2, "status needs one element")
-    return _want("status", status, torch.int32, status.shape, dev)
+    return _want("status", status, _torch_module.int32, status.shape, dev)
 
 
-def _out(name, t, dtype, shape, dev, stream):
-    """(tensor, address) of an output: t checked, or a new one.  New memory belongs to the call's stream, so that
-    it is reused in that stream's order."""
-    import torch
+def _out(name, t, like, dtype, shape, dev, stream):
+    """(tensor, address) of an output: t checked, or a new one on like's device.  New memory belongs to the call's
+    stream, so that it is reused in that stream's order."""
     if t is not None:
         return t, _want(name, t, dtype, shape, dev)
     if stream is None:
-        t = torch.empty(shape, dtype=dtype, device="cuda")
+        t = like.new_empty(shape, dtype=dtype)
     else:
-        with torch.cuda.stream(stream):
-            t = torch.empty(shape, dtype=dtype, device="cuda")
+        with _torch_module.cuda.stream(stream):
+            t = like.new_empty(shape, dtype=dtype)
     return t, t.data_ptr()
 
 
 def _latent_cache(cache, block_table, n_seqs, dev):
-    import torch
+    torch = _torch_module
     if cache.dim() != 3 or block_table.dim() != 2:
         raise TpcError(2, f"cache must be [n_pages, page_size, {LATENT_WIDTH}] and block_table [n_seqs, max_pages], got "
                           f"{tuple(cache.shape)} and {tuple(block_table.shape)}")
@@ -910,10 +918,9 @@ def _latent_cache(cache, block_table, n_seqs, dev):
 
 def _kv_len(kv_len, dev):
     """(address, sequences) of the cached lengths."""
-    import torch
     if kv_len.dim() != 1:
         raise TpcError(2, f"kv_len must be [n_seqs], got {tuple(kv_len.shape)}")
-    return _want("kv_len", kv_len, torch.int32, kv_len.shape, dev), kv_len.shape[0]
+    return _want("kv_len", kv_len, _torch_module.int32, kv_len.shape, dev), kv_len.shape[0]
 
 
 def tpc_kda_step(state, src, q, k, v, g, beta, dst=None, row_start=None, out_dtype=None, o=None, status=None,
@@ -921,7 +928,7 @@ def tpc_kda_step(state, src, q, k, v, g, beta, dst=None, row_start=None, out_dty
     """Advances cached KDA states by the batch's new rows (include/tpc.h); returns o [n_rows, H, d].
     state: fp32 [n_slots, H, d, d], updated; src: int32 [n_seqs] slot read by each sequence; dst: slot written
     (default: in place); row_start: int32 [n_seqs + 1] rows of each sequence (default: one each)."""
-    import torch
+    torch = _torch()
     dev = _decode_device(state)
     if q.dim() != 3 or state.dim() != 4 or src.dim() != 1:
         raise TpcError(2, f"q must be [n_rows, H, d], state [n_slots, H, d, d] and src [n_seqs], got {tuple(q.shape)}, "
@@ -933,15 +940,16 @@ def tpc_kda_step(state, src, q, k, v, g, beta, dst=None, row_start=None, out_dty
     bf, f32 = torch.bfloat16, torch.float32
     if (dt is not bf and dt is not f32) or (out_dtype is not bf and out_dtype is not f32):
         raise TpcError(2, f"rows and outputs are bf16 or fp32, got {dt} and {out_dtype}")
-    p = [_want(name, t, dt, rows, dev) for name, t in (("q", q), ("k", k), ("v", v), ("g", g))]
+    p_q, p_k = _want("q", q, dt, rows, dev), _want("k", k, dt, rows, dev)
+    p_v, p_g = _want("v", v, dt, rows, dev), _want("g", g, dt, rows, dev)
     p_beta, p_state = _want("beta", beta, dt, (n, H), dev), _want("state", state, f32, (n_slots, H, d, d), dev)
     p_src = _want("src", src, i32, (n_seqs,), dev)
     p_dst = 0 if dst is None else _want("dst", dst, i32, (n_seqs,), dev)
     batch = _decode_rows(n, row_start, 0, n_seqs, dev)
     status = _status(status, dev)
-    o, p_o = _out("o", o, out_dtype, rows, dev, stream)
+    o, p_o = _out("o", o, q, out_dtype, rows, dev, stream)
     _check(lib().tpc_kda_step(_pack_shape(H, d, d, dt is bf, out_dtype is bf), batch,
-                              _pack_step(*p, p_beta, p_state, n_slots, p_src, p_dst, p_o), status,
+                              _pack_step(p_q, p_k, p_v, p_g, p_beta, p_state, n_slots, p_src, p_dst, p_o), status,
                               _decode_stream(stream, dev)))
     return o
 
@@ -950,7 +958,7 @@ def tpc_latent_append(cache, block_table, kv_len, c, kr, row_start=None, status=
     """Writes the new rows' latents and rotated keys into the paged cache (include/tpc.h).  cache: bf16 [n_pages,
     page_size, 576]; block_table: int32 [n_seqs, max_pages]; kv_len: int32 [n_seqs], new rows included; c [n_rows,
     512] and kr [n_rows, 64]: bf16 or fp32, rows may be slices of a wider tensor."""
-    import torch
+    torch = _torch()
     dev = _decode_device(cache)
     p_kv, n_seqs = _kv_len(kv_len, dev)
     lc = _latent_cache(cache, block_table, n_seqs, dev)
@@ -968,8 +976,7 @@ def tpc_latent_append(cache, block_table, kv_len, c, kr, row_start=None, status=
 def tpc_latent_absorb(q, w_b, kv_len, row_start=None, qa=None, status=None, stream=None):
     """Absorbed queries qa [n_rows, H, 576] (bf16) of q [n_rows, H, 192] (bf16; the rows may be slices of a wider
     tensor) and the group's w_b [2 * 128 * H, 512], the rotary part turned at the rows' positions (include/tpc.h)."""
-    import torch
-    dev, bf = _decode_device(q), torch.bfloat16
+    dev, bf = _decode_device(q), _torch_module.bfloat16
     p_kv, n_seqs = _kv_len(kv_len, dev)
     if q.dim() != 3:
         raise TpcError(2, f"q must be [n_rows, H, {LATENT_HEAD + LATENT_ROPE}], got {tuple(q.shape)}")
@@ -978,22 +985,27 @@ def tpc_latent_absorb(q, w_b, kv_len, row_start=None, qa=None, status=None, stre
     p_w = _want("w_b", w_b, bf, (2 * LATENT_HEAD * H, LATENT_DIM), dev)
     batch = _decode_rows(n, row_start, p_kv, n_seqs, dev)
     status = _status(status, dev)
-    qa, p_qa = _out("qa", qa, bf, (n, H, LATENT_WIDTH), dev, stream)
+    qa, p_qa = _out("qa", qa, q, bf, (n, H, LATENT_WIDTH), dev, stream)
     _check(lib().tpc_latent_absorb(batch, H, p_q, ld_q, p_w, p_qa, status, _decode_stream(stream, dev)))
     return qa
 
 
+@functools.lru_cache(maxsize=None)
+def _scratch_bytes(H):
+    return int(lib().tpc_latent_attn_scratch_bytes(H))
+
+
 def latent_attn_scratch(H, device="cuda"):
     """Scratch of tpc_latent_attn for H heads (used by one call at a time)."""
-    import torch
-    return torch.empty(int(lib().tpc_latent_attn_scratch_bytes(H)), dtype=torch.uint8, device=device)
+    torch = _torch()
+    return torch.empty(_scratch_bytes(H), dtype=torch.uint8, device=device)
 
 
 def tpc_latent_attn(qa, cache, block_table, kv_len, scale, row_start=None, o=None, lse=None, scratch=None,
                     status=None, stream=None):
     """Absorbed latent attention of the new rows over the paged cache (include/tpc.h); returns (o [n_rows, H, 512]
     bf16, lse [n_rows, H] fp32).  qa: bf16 [n_rows, H, 576] of tpc_latent_absorb."""
-    import torch
+    torch = _torch()
     dev, bf = _decode_device(qa), torch.bfloat16
     p_kv, n_seqs = _kv_len(kv_len, dev)
     if qa.dim() != 3:
@@ -1003,10 +1015,10 @@ def tpc_latent_attn(qa, cache, block_table, kv_len, scale, row_start=None, o=Non
     lc = _latent_cache(cache, block_table, n_seqs, dev)
     batch = _decode_rows(n, row_start, p_kv, n_seqs, dev)
     status = _status(status, dev)
-    need = int(lib().tpc_latent_attn_scratch_bytes(H)) if scratch is None else scratch.numel()
-    scratch, p_scratch = _out("scratch", scratch, torch.uint8, (need,), dev, stream)
-    o, p_o = _out("o", o, bf, (n, H, LATENT_DIM), dev, stream)
-    lse, p_lse = _out("lse", lse, torch.float32, (n, H), dev, stream)
+    need = _scratch_bytes(H) if scratch is None else scratch.numel()
+    scratch, p_scratch = _out("scratch", scratch, qa, torch.uint8, (need,), dev, stream)
+    o, p_o = _out("o", o, qa, bf, (n, H, LATENT_DIM), dev, stream)
+    lse, p_lse = _out("lse", lse, qa, torch.float32, (n, H), dev, stream)
     _check(lib().tpc_latent_attn(lc, batch, H, scale, p_qa, p_o, p_lse, p_scratch, need, status,
                                  _decode_stream(stream, dev)))
     return o, lse
@@ -1014,13 +1026,12 @@ def tpc_latent_attn(qa, cache, block_table, kv_len, scale, row_start=None, o=Non
 
 def tpc_latent_expand(o, w_b, out=None, status=None, stream=None):
     """Head outputs [n_rows, H, 128] (bf16) of the attention's o [n_rows, H, 512] through w_b's value rows."""
-    import torch
-    dev, bf = _decode_device(o), torch.bfloat16
+    dev, bf = _decode_device(o), _torch_module.bfloat16
     if o.dim() != 3:
         raise TpcError(2, f"o must be [n_rows, H, {LATENT_DIM}], got {tuple(o.shape)}")
     n, H, _ = o.shape
     p_x, p_w = _want("o", o, bf, (n, H, LATENT_DIM), dev), _want("w_b", w_b, bf, (2 * LATENT_HEAD * H, LATENT_DIM), dev)
     status = _status(status, dev)
-    out, p_out = _out("out", out, bf, (n, H, LATENT_HEAD), dev, stream)
+    out, p_out = _out("out", out, o, bf, (n, H, LATENT_HEAD), dev, stream)
     _check(lib().tpc_latent_expand(n, H, p_x, p_w, p_out, status, _decode_stream(stream, dev)))
     return out

@@ -65,6 +65,10 @@ struct LatAttnArgs {
 struct LatSeq {
   int row0, m, kv;
 };
+struct LatStart {  // where a share begins
+  int b, ct, tile;
+  LatSeq s;
+};
 
 __device__ __forceinline__ LatSeq lat_seq(const LatAttnArgs& a, int b) {
   LatSeq s;
@@ -101,13 +105,9 @@ struct LatWalk {
   long long left;
   int b, ct, t0, n, tiles;
   LatSeq s;
-  __device__ LatWalk(const LatAttnArgs& args, int b0, int ct0, int tile0, long long count)
-      : a(args), left(count), b(b0), ct(ct0), t0(tile0), n(0), tiles(0) {
-    if (left > 0) enter();
-  }
-  __device__ void enter() {
-    s = lat_seq(a, b);
-    size();
+  __device__ LatWalk(const LatAttnArgs& args, const LatStart& at, long long count)
+      : a(args), left(count), b(at.b), ct(at.ct), t0(at.tile), n(0), tiles(0), s(at.s) {
+    if (left > 0) size();
   }
   __device__ void size() {
     tiles = lat_tiles<NT>(a, s, ct);
@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
            *q_full = bars + 18, *q_empty = bars + 19, *done = bars + 20;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 21);
   int* abort_flag = reinterpret_cast<int*>(bars + 21) + 1;
-  int* where = reinterpret_cast<int*>(bars + 22);             // b, ct, tile of the share's start
-  long long* sums = reinterpret_cast<long long*>(bars + 24);  // per warp
+  LatStart* where = reinterpret_cast<LatStart*>(bars + 22);
+  long long* sums = reinterpret_cast<long long*>(bars + 25);  // per warp
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     prefetch_tensor_map(&tma_kv);
@@ -282,11 +282,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < n; ++c) {
         const int t = lat_tiles<NT>(a, s, c);
-        if (at >= 0 && at < t) {
-          where[0] = b;
-          where[1] = c;
-          where[2] = (int)at;
-        }
+        if (at >= 0 && at < t) *where = {b, c, (int)at, s};
         at -= t;
       }
     }
@@ -294,7 +290,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // latent_combine_kernel waits for this grid's end itself
   const uint32_t tb = *tslot;
-  LatWalk<NT> walk(a, where[0], where[1], where[2], share);
+  LatWalk<NT> walk(a, *where, share);
   auto aborted = [&] { return *((volatile int*)abort_flag) != 0; };
   // Every wait is bounded.  After the first that runs out no role waits, copies or multiplies any
   // more, but all walk on to the end of their loops, so the barriers between the softmax warps match.
@@ -343,9 +339,10 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       const int my_row = cur.page * ps + cur.off;
       if (cur.first) {
         ++piece;
-        if ((piece == 0 || wait(q_empty, (piece - 1) & 1)) && lane == 0) {
-          mbar_arrive_expect_tx(q_full, kLatChunks * NT * 128);
-          for (int c = 0; c < kLatChunks; ++c) tma_load_2d(sm + L::q + c * NT * 128, &tma_q, 64 * c, cur.q_row, q_full);
+        if (__all_sync(0xffffffffu, piece == 0 || wait(q_empty, (piece - 1) & 1))) {
+          if (lane == 0) mbar_arrive_expect_tx(q_full, kLatChunks * NT * 128);
+          __syncwarp();
+          if (lane < kLatChunks) tma_load_2d(sm + L::q + lane * NT * 128, &tma_q, 64 * lane, cur.q_row, q_full);
         }
       }
       for (int e = 0; e < kLatItems; ++e, ++item) {
