@@ -645,12 +645,31 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
 // Joins the pieces of every unit that starts in one share and ends in a later one:
 //   o = sum_i e^{m_i - m} O_i / sum_i e^{m_i - m} l_i,
 // in an order that depends on the number of pieces alone.  Launched while the attention kernel still
-// runs (it waits for that grid's end).  The CTAs share a list of work items: a ragged batch leaves a
-// unit per share with two or three pieces (item: four columns, a group of 128 threads each, thread = 4
-// dimensions), one long context a single unit with a piece per share (item: 128 dimensions of one
-// column, 16 warps with every 16th piece each, so that the loads overlap).  One CTA per column
-// instead: 64 x 16384 tokens 11.5 us and one context of 65536 19.7 us.
-constexpr int kLatCombThreads = 512, kLatCombFew = 8;
+// runs (it waits for that grid's end).  Its time is that of a chain of loads, so a thread takes at most
+// 8 to 10 pieces, all loaded at once, and the CTAs share a list of work items of three kinds:
+//   up to 8 pieces (ragged batches, most units): four columns, 128 threads x 4 dimensions each;
+//   up to 32 (a few contexts): one column, a group of 128 threads for every fourth piece;
+//   more (one context over all CTAs): 128 dimensions of a column, a warp for every 16th piece.
+// With one CTA per column instead, one context of 6000 tokens took 21.6 us of joining, and with the last
+// kind for everything above 8 pieces, 64 columns of 8 contexts of 4000 tokens 33 us.
+constexpr int kLatCombThreads = 512, kLatCombFew = 8, kLatCombSome = 32;
+
+struct LatJoin {  // running sum of pieces for 4 dimensions of a column
+  float4 o;
+  __device__ __forceinline__ void add(float e, const float4& x) {
+    o.x = fmaf(e, x.x, o.x);
+    o.y = fmaf(e, x.y, o.y);
+    o.z = fmaf(e, x.z, o.z);
+    o.w = fmaf(e, x.w, o.w);
+  }
+  __device__ __forceinline__ void store(const LatAttnArgs& a, size_t col, int d, float m, float l) const {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+    store4(a.o + col * kLatDim + d, v);
+    if (d == 0) a.lse[col] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
+};
+
 __global__ void __launch_bounds__(kLatCombThreads) latent_combine_kernel(LatAttnArgs a, int shares) {
   __shared__ LatPiece unit[kLatMaxCtas];
   __shared__ int ends[kLatMaxCtas];  // items of units 0 .. i
@@ -661,8 +680,9 @@ __global__ void __launch_bounds__(kLatCombThreads) latent_combine_kernel(LatAttn
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int cnt = 0;
   if (tid < shares) {
-    unit[tid] = a.meta[tid];
-    cnt = unit[tid].n == 0 ? 0 : unit[tid].n <= kLatCombFew ? (unit[tid].ncols + 3) / 4 : 4 * unit[tid].ncols;
+    const LatPiece u = a.meta[tid];
+    unit[tid] = u;
+    cnt = u.n == 0 ? 0 : u.n <= kLatCombFew ? (u.ncols + 3) / 4 : u.n <= kLatCombSome ? u.ncols : 4 * u.ncols;
   }
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -682,12 +702,13 @@ __global__ void __launch_bounds__(kLatCombThreads) latent_combine_kernel(LatAttn
     const LatPiece u = unit[s];
     const int k = item - (s ? ends[s - 1] : 0);
     auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * s + 1 : 2 * (s + i)) * kLatMaxNT; };
+    LatJoin join{make_float4(0.f, 0.f, 0.f, 0.f)};
     if (u.n <= kLatCombFew) {
       const int c = 4 * k + (tid >> 7), d = 4 * (tid & 127);
       if (c >= u.ncols) continue;
       float m = -INFINITY, l = 0.f;
       float2 ml[kLatCombFew];
-      float4 x[kLatCombFew], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 x[kLatCombFew];
 #pragma unroll
       for (int i = 0; i < kLatCombFew; ++i)
         if (i < u.n) {
@@ -701,18 +722,15 @@ __global__ void __launch_bounds__(kLatCombThreads) latent_combine_kernel(LatAttn
         if (i < u.n) {
           const float e = tc::ex2(ml[i].x - m);
           l = fmaf(e, ml[i].y, l);
-          acc.x = fmaf(e, x[i].x, acc.x);
-          acc.y = fmaf(e, x[i].y, acc.y);
-          acc.z = fmaf(e, x[i].z, acc.z);
-          acc.w = fmaf(e, x[i].w, acc.w);
+          join.add(e, x[i]);
         }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-      store4(a.o + ((size_t)u.col0 + c) * kLatDim + d, o);
-      if (d == 0) a.lse[u.col0 + c] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      join.store(a, (size_t)u.col0 + c, d, m, l);
       continue;
     }
-    const int c = k >> 2, d = 128 * (k & 3) + 4 * lane;
+    // G groups of threads, group g takes pieces g, g + G, ...; d: the thread's dimensions
+    const bool some = u.n <= kLatCombSome;
+    const int c = some ? k : k >> 2, d = some ? 4 * (tid & 127) : 128 * (k & 3) + 4 * lane;
+    const int G = some ? kLatCombThreads / 128 : kLatCombThreads / 32, g = some ? tid >> 7 : w;
     float m = -INFINITY, l = 0.f;
     for (int i = lane; i < u.n; i += 32) m = fmaxf(m, a.ml[slot(i) + c].x);
 #pragma unroll
@@ -727,31 +745,16 @@ __global__ void __launch_bounds__(kLatCombThreads) latent_combine_kernel(LatAttn
 #pragma unroll
     for (int e = 16; e; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
     __syncthreads();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 5
-    for (int i = w; i < u.n; i += kLatCombThreads / 32) {
-      const float4 x = *reinterpret_cast<const float4*>(a.part + (slot(i) + c) * kLatDim + d);
-      const float e = f[i];
-      acc.x = fmaf(e, x.x, acc.x);
-      acc.y = fmaf(e, x.y, acc.y);
-      acc.z = fmaf(e, x.z, acc.z);
-      acc.w = fmaf(e, x.w, acc.w);
-    }
-    acc_s[tid] = acc;
+    for (int i = g; i < u.n; i += G)
+      join.add(f[i], *reinterpret_cast<const float4*>(a.part + (slot(i) + c) * kLatDim + d));
+    acc_s[tid] = join.o;
     __syncthreads();
-    if (w == 0) {
-#pragma unroll
-      for (int i = 1; i < kLatCombThreads / 32; ++i) {
-        const float4 x = acc_s[32 * i + lane];
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
-      }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-      store4(a.o + ((size_t)u.col0 + c) * kLatDim + d, o);
-      if (d == 0) a.lse[u.col0 + c] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    if (g == 0) {
+      const int step = kLatCombThreads / G;
+#pragma unroll 3
+      for (int i = 1; i < G; ++i) join.add(1.f, acc_s[step * i + tid]);
+      join.store(a, (size_t)u.col0 + c, d, m, l);
     }
     __syncthreads();  // f and acc_s are free again
   }
