@@ -594,7 +594,8 @@ typedef struct tpc_latent_cache {
  *   (TPC_F32 or TPC_BF16); 16-byte aligned, leading dimensions multiples of 16 bytes, so that both
  *   may be slices of a projection.
  * Rows without a token are skipped.  Two rows that write one cached token (a page of two
- * sequences that both write it) race: with a status word that records TPC_ERR_DEVICE_CHECK.
+ * sequences that both write it) race: with a status word that records TPC_ERR_DEVICE_CHECK (a
+ * comparison of every written page with every other one of the batch).
  */
 int tpc_latent_append(const tpc_latent_cache* cache, const tpc_rows* rows, const void* c, int64_t ld_c,
                       const void* kr, int64_t ld_kr, int32_t in_dtype, int32_t* status, tpc_stream_t stream);
@@ -616,7 +617,8 @@ int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld
  *   o[t][h] = sum_j softmax_j(scale qa[t][h] . cache_j) c_j   (bf16 [n_rows][H][512]),
  *   lse[t][h] = log sum_j exp(scale qa[t][h] . cache_j)        (fp32 [n_rows][H], natural log).
  * A row without a token gets o = 0 and lse = -infinity.  Tokens past kv_len are never used,
- * whatever the page holds there.  Scores, softmax statistics and sums in fp32; the weights enter
+ * whatever the page holds there; a latent that is not finite among the kv_len tokens can make any row
+ * of its sequence NaN, rows before it included.  Scores, softmax statistics and sums in fp32; the weights enter
  * their product as bf16.  qa: [n_rows][H][576] bf16, 16-byte aligned, 1 <= H <= 128.
  *   scratch: tpc_latent_attn_scratch_bytes(H) bytes, 256-byte aligned, used by one call at a time.
  * Deterministic: the same call gives the same bits.  A block table entry outside 0 .. n_pages - 1

@@ -1019,7 +1019,7 @@ def tpc_latent_attn(qa, cache, block_table, kv_len, scale, row_start=None, o=Non
     scratch, p_scratch = _out("scratch", scratch, qa, torch.uint8, (need,), dev, stream)
     o, p_o = _out("o", o, qa, bf, (n, H, LATENT_DIM), dev, stream)
     lse, p_lse = _out("lse", lse, qa, torch.float32, (n, H), dev, stream)
-    _check(lib().tpc_latent_attn(lc, batch, H, scale, p_qa, p_o, p_lse, p_scratch, need, status,
+    _check(lib().tpc_latent_attn(lc, batch, H, float(scale), p_qa, p_o, p_lse, p_scratch, need, status,
                                  _decode_stream(stream, dev)))
     return o, lse
 

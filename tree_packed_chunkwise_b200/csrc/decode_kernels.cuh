@@ -144,15 +144,16 @@ __global__ void __launch_bounds__(kStepThreads, StepShape<D>::per_sm) kda_step_k
     if (lane == 0) set_status(a.status, kStatusCheck);
     return;
   }
-  // one warp per sequence looks for another sequence that writes or reads the slot it writes
+  // one warp per sequence looks for another sequence that writes or reads the slot it writes (in place,
+  // a later one: the earlier ones look themselves)
   if (a.status && h == 0 && sl == 0) {
     bool clash = false;
-    for (int j = lane; j < a.rows.n_seqs; j += 32) {
+#pragma unroll 4
+    for (int j = (a.dst ? 0 : b + 1) + lane; j < a.rows.n_seqs; j += 32) {
       const int sj = a.src[j];
-      if (j == b || sj < 0) continue;
-      clash |= sj == dst || (a.dst && a.dst[j] == dst);
+      clash |= j != b && sj >= 0 && (sj == dst || (a.dst && a.dst[j] == dst));
     }
-    if (__any_sync(0xffffffffu, clash) && lane == 0) set_status(a.status, kStatusCheck);
+    if (clash) set_status(a.status, kStatusCheck);
   }
   const int r0 = rg * R, c0 = (sl * CG + lane % CG) * 4;
   const size_t at = (size_t)r0 * D + c0;
@@ -251,21 +252,28 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendArg
   rope_angle(r.pos, lane, &cs, &sn);
   dst[kLatDim + lane] = __float2bfloat16_rn(x * cs - y * sn);
   dst[kLatDim + 32 + lane] = __float2bfloat16_rn(x * sn + y * cs);
-  // a page that two sequences both write: the first of this row's run in the page compares the
-  // (sequence, page) pairs of the batch
+  // a page that two sequences both write: the first row of this run in the page compares it with the
+  // pages that its own and later sequences write after it, a sequence per lane
   if (!a.status) return;
-  const int first = a.rows.row_start ? a.rows.row_start[r.seq] : t;
-  if (t != first && r.pos % a.cache.page_size) return;
+  const int first = a.rows.row_start ? a.rows.row_start[r.seq] : t, ps = a.cache.page_size;
+  if (t != first && r.pos % ps) return;
   bool clash = false;
-  for (int s = 0; s < a.rows.n_seqs; ++s) {
-    const int m = a.rows.row_start ? a.rows.row_start[s + 1] - a.rows.row_start[s] : 1;
-    const int64_t kv = a.rows.kv_len[s], p0 = max((int64_t)0, kv - m) / a.cache.page_size;
-    const int64_t p1 = min((kv + a.cache.page_size - 1) / a.cache.page_size, (int64_t)a.cache.max_pages);
-    if (m <= 0) continue;
-    for (int64_t p = p0 + lane; p < p1; p += 32)
-      clash |= !(s == r.seq && p == pg) && a.cache.table[(size_t)s * a.cache.max_pages + p] == page;
+  if (!a.rows.row_start) {
+#pragma unroll 4
+    for (int s = r.seq + 1 + lane; s < a.rows.n_seqs; s += 32) {
+      const int p = max(a.rows.kv_len[s] - 1, 0) / ps;
+      clash |= a.rows.kv_len[s] > 0 && p < a.cache.max_pages && a.cache.table[(size_t)s * a.cache.max_pages + p] == page;
+    }
+  } else {
+    for (int s = r.seq + lane; s < a.rows.n_seqs; s += 32) {
+      const int64_t m = (int64_t)a.rows.row_start[s + 1] - a.rows.row_start[s];
+      const int kv = min(max(a.rows.kv_len[s], 0), a.cache.max_pages * ps), p1 = (kv + ps - 1) / ps;
+      if (m <= 0) continue;
+      for (int p = s == r.seq ? (int)pg + 1 : (int)(max((int64_t)0, kv - m) / ps); p < p1; ++p)
+        clash |= a.cache.table[(size_t)s * a.cache.max_pages + p] == page;
+    }
   }
-  if (__any_sync(0xffffffffu, clash) && lane == 0) set_status(a.status, kStatusCheck);
+  if (clash) set_status(a.status, kStatusCheck);
 }
 
 // ------------------------------------------------------------------------------------ rotated queries

@@ -646,13 +646,14 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
 //   o = sum_i e^{m_i - m} O_i / sum_i e^{m_i - m} l_i,
 // in an order that depends on the number of pieces alone.  Launched while the attention kernel still
 // runs (it waits for that grid's end).  Its time is that of a chain of loads, so a thread takes at most
-// 8 to 10 pieces, all loaded at once, and the CTAs share a list of work items of three kinds:
-//   up to 8 pieces (ragged batches, most units): four columns, 128 threads x 4 dimensions each;
+// 4 to 10 pieces, mostly loaded at once, and the CTAs share a list of work items of three kinds:
+//   up to 4 pieces (ragged batches, most units): four columns, 128 threads x 4 dimensions each;
 //   up to 32 (a few contexts): one column, a group of 128 threads for every fourth piece;
 //   more (one context over all CTAs): 128 dimensions of a column, a warp for every 16th piece.
-// With one CTA per column instead, one context of 6000 tokens took 21.6 us of joining, and with the last
-// kind for everything above 8 pieces, 64 columns of 8 contexts of 4000 tokens 33 us.
-constexpr int kLatCombThreads = 512, kLatCombFew = 8, kLatCombSome = 32;
+// Whole calls of 8 contexts of 4000 tokens with 64 columns: 25.2 us; with up to 8 pieces a thread (one CTA
+// an SM for its registers) 30.4, with the last kind for all above 8 pieces 46.  One context of 6000
+// tokens: 14 us, and 34 with one CTA per column.
+constexpr int kLatCombThreads = 512, kLatCombFew = 4, kLatCombSome = 32;
 
 struct LatJoin {  // running sum of pieces for 4 dimensions of a column
   float4 o;
@@ -670,7 +671,7 @@ struct LatJoin {  // running sum of pieces for 4 dimensions of a column
   }
 };
 
-__global__ void __launch_bounds__(kLatCombThreads) latent_combine_kernel(LatAttnArgs a, int shares) {
+__global__ void __launch_bounds__(kLatCombThreads, 2) latent_combine_kernel(LatAttnArgs a, int shares) {
   __shared__ LatPiece unit[kLatMaxCtas];
   __shared__ int ends[kLatMaxCtas];  // items of units 0 .. i
   __shared__ int part_sum[kLatCombThreads / 32];
