@@ -53,10 +53,16 @@ __device__ __forceinline__ RowAt row_at(const DecodeRows& r, int t) {
   return {b, (int64_t)r.kv_len[b] - r.row_start[b + 1] + t};
 }
 
-// cos and sin of pos * 10000^(-2 i / 64).  The angle is taken in turns in double precision and reduced
+// 10000^(-2 i / 64) / (2 pi): turns per position of the rotary pair i (computed once on the host; a
+// kernel parameter, so that no thread evaluates a power)
+struct RopeTurns {
+  double t[kLatRope / 2];
+};
+
+// cos and sin of the angle at position pos.  The angle is taken in turns in double precision and reduced
 // there (2^31 positions: error below 1e-6 of a turn), so that far positions keep fp32 accuracy.
-__device__ __forceinline__ void rope_angle(int64_t pos, int i, float* cs, float* sn) {
-  const double turns = (double)pos * (exp2(-(double)i * (13.287712379549449 / (kLatRope / 2))) * 0.15915494309189535);
+__device__ __forceinline__ void rope_angle(int64_t pos, double per_pos, float* cs, float* sn) {
+  const double turns = (double)pos * per_pos;
   sincospif(2.f * (float)(turns - rint(turns)), sn, cs);
 }
 
@@ -214,6 +220,7 @@ struct AppendArgs {
   const void *c, *kr;
   int64_t ld_c, ld_kr;
   int* status;
+  RopeTurns rope;
 };
 
 constexpr int kAppendThreads = 128;
@@ -221,7 +228,7 @@ constexpr int kAppendThreads = 128;
 // One warp per row: 16 latent elements per lane, then lane i turns the pair (i, i + 32) of the
 // rotary key.  Bound by the row's bytes; each is read and written once.
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __grid_constant__ AppendArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t t64 = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   if (t64 >= a.rows.n_rows) return;
@@ -249,7 +256,7 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendArg
   }
   const float x = to_f(kr[lane]), y = to_f(kr[lane + 32]);
   float cs, sn;
-  rope_angle(r.pos, lane, &cs, &sn);
+  rope_angle(r.pos, a.rope.t[lane], &cs, &sn);
   dst[kLatDim + lane] = __float2bfloat16_rn(x * cs - y * sn);
   dst[kLatDim + 32 + lane] = __float2bfloat16_rn(x * sn + y * cs);
   // a page that two sequences both write: the first row of this run in the page compares it with the
@@ -279,31 +286,39 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendArg
 // ------------------------------------------------------------------------------------ rotated queries
 // The rotary part of the absorbed queries: a warp turns every head of one row.  Lane i takes cos and sin of
 // angle i; then four lanes hold a head (8 neighbouring pairs each), eight heads at a time.
-__device__ __forceinline__ void absorb_rope_row(const DecodeRows& rows, int H, const __nv_bfloat16* q, int64_t ld_q,
-                                                __nv_bfloat16* qa, int t) {
+__device__ __forceinline__ void absorb_rope_row(const DecodeRows& rows, const RopeTurns& rope, int H,
+                                                const __nv_bfloat16* q, int64_t ld_q, __nv_bfloat16* qa, int t) {
   const int lane = threadIdx.x & 31, j0 = (lane & 3) * 8;
+  const __nv_bfloat16* src = q + (size_t)t * ld_q + kLatHead + j0;
+  uint4 x4, y4;  // the first heads, loaded before the position is known
+  int h = lane >> 2;
+  auto load = [&] {
+    const uint4* p = reinterpret_cast<const uint4*>(src + (size_t)h * kLatQK);
+    x4 = p[0];
+    y4 = p[4];
+  };
+  if (h < H) load();
   const RowAt r = row_at(rows, t);
   if (r.seq < 0) return;
   float cs, sn, c[8], s[8];
-  rope_angle(r.pos, lane, &cs, &sn);
+  rope_angle(r.pos, rope.t[lane], &cs, &sn);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     c[j] = __shfl_sync(0xffffffffu, cs, j0 + j);
     s[j] = __shfl_sync(0xffffffffu, sn, j0 + j);
   }
-#pragma unroll 2
-  for (int h = lane >> 2; h < H; h += 8) {
-    const __nv_bfloat16* src = q + (size_t)t * ld_q + (size_t)h * kLatQK + kLatHead + j0;
-    __nv_bfloat16* dst = qa + ((size_t)t * H + h) * kLatWidth + kLatDim + j0;
-    float x[8], y[8];
-    load_vec<__nv_bfloat16, 8>(src, x);
-    load_vec<__nv_bfloat16, 8>(src + 32, y);
+  while (h < H) {
+    const __nv_bfloat16 *x = reinterpret_cast<const __nv_bfloat16*>(&x4), *y = reinterpret_cast<const __nv_bfloat16*>(&y4);
     __align__(16) __nv_bfloat16 u[8], v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      u[j] = __float2bfloat16_rn(x[j] * c[j] - y[j] * s[j]);
-      v[j] = __float2bfloat16_rn(x[j] * s[j] + y[j] * c[j]);
+      const float xf = to_f(x[j]), yf = to_f(y[j]);
+      u[j] = __float2bfloat16_rn(xf * c[j] - yf * s[j]);
+      v[j] = __float2bfloat16_rn(xf * s[j] + yf * c[j]);
     }
+    __nv_bfloat16* dst = qa + ((size_t)t * H + h) * kLatWidth + kLatDim + j0;
+    h += 8;
+    if (h < H) load();
     *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(u);
     *reinterpret_cast<uint4*>(dst + 32) = *reinterpret_cast<const uint4*>(v);
   }

@@ -793,19 +793,22 @@ __global__ void __launch_bounds__(kLatCombThreads, 2) latent_combine_kernel(LatA
 
 // ------------------------------------------------------------------------------------ per-head products
 // The absorbed queries qa[t][h][l] = sum_i q[t][h][i] W_k[h][i][l] (K = 128, 512 outputs) and their rotary
-// part.  Bound by writing qa (the weights and q are read from L2 after their first use).  A CTA takes 128
-// rows of a head and `blocks` of the four 128-wide output blocks: the rows stay in shared memory, the
-// weights (stored [i][l], MN-major) follow in steps of 64 i, and two accumulators alternate, so that
-// rounding and writing a block overlaps the next block's loads and MMAs.  Two CTAs share an SM.  Four
-// blocks a CTA once that fills every SM twice, two once it fills them (16 heads, us with 1 / 2 / 4 blocks:
-// 96 rows 4.3 / 5.1 / 7.4, 640 rows 8.2 / 7.7 / 8.4, 1300 rows 12.1 / 10.8 / 11.9, 4096 rows 37.8 / 28.5 /
-// 26.6, that is 3.86 TB/s).  The rotary parts of all rows are spread over the CTAs' writing warps.
-constexpr int kHeadTcThreads = 192;
+// part.  Bound by writing qa (the weights and q are read from L2 after their first use).  The work is one
+// list of blocks (128 rows, head, 128 outputs), outputs fastest, and a CTA takes `blocks` consecutive ones:
+// the rows stay in shared memory while their four output blocks go by, the weights (stored [i][l],
+// MN-major) follow in steps of 64 i, and two accumulators alternate, so that rounding and writing a block
+// overlaps the loads and MMAs of the next one.  Two CTAs share an SM, one block each while that is
+// all there is.  The rotary parts of all rows are spread over the CTAs' writing warps, between blocks.
+// 4096 rows of 16 heads: 24.5 us (4.2 TB/s; without the stores 11.6, without the rotary parts 20.8); every
+// CTA a tile of its own 26.6 (four output blocks) and 37.8 us (one); one CTA an SM with its head's weights
+// resident and sixteen writing warps 28.0 us: the chains of loads of a single CTA are not hidden.
+constexpr int kAbsorbThreads = 320;  // producer warp, MMA warp, eight writing warps
+constexpr int kAbsorbPerSm = 2;
 
 struct AbsorbSmem {
   static constexpr int w_slots = 3;
-  static constexpr uint32_t x = 2 * 128 * 128, w = 64 * 256, out_ld = 64 * 2 + 16;
-  static constexpr uint32_t out = x + w_slots * w, total = out + 128 * out_ld + 1024;  // + slack to align the tiles
+  static constexpr uint32_t x = 2 * 128 * 128, w = 64 * 256, out_ld = 32 * 2 + 16;
+  static constexpr uint32_t out = x + w_slots * w, total = out + 8 * 32 * out_ld + 1024;  // + slack to align the tiles
 };
 
 struct AbsorbArgs {
@@ -815,23 +818,32 @@ struct AbsorbArgs {
   int64_t ld_q;
   __nv_bfloat16* qa;
   int* status;
-  int blocks;  // output blocks per CTA: 1, 2 or 4
+  int64_t total;  // blocks in all, and of one CTA
+  int blocks;
+  RopeTurns rope;
 };
 
-__global__ void __launch_bounds__(kHeadTcThreads)
-    latent_absorb_tc(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, AbsorbArgs a) {
+__global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
+    latent_absorb_tc(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w,
+                     const __grid_constant__ AbsorbArgs a) {
   using namespace tc;
   using L = AbsorbSmem;
   extern __shared__ __align__(1024) uint8_t hsm_raw[];
   uint8_t* sm = hsm_raw + ((1024u - (smem_u32(hsm_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t x_full[2], w_full[L::w_slots], w_empty[L::w_slots], acc_full[2], acc_empty[2];
+  __shared__ __align__(8) uint64_t x_full, x_empty, w_full[L::w_slots], w_empty[L::w_slots], acc_full[2], acc_empty[2];
   __shared__ uint32_t tslot;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  // tile order: output blocks, then heads, fastest, so that CTAs in flight read the same rows
-  int tile = (int)blockIdx.x;
-  const int per_head = kLatDim / 128 / a.blocks, nb0 = tile % per_head * a.blocks;
-  tile /= per_head;
-  const int h = tile % a.H, t0 = tile / a.H * 128;
+  constexpr int kOut = kLatDim / 128;  // output blocks of a (rows, head) pair
+  const int64_t first = (int64_t)blockIdx.x * a.blocks;
+  const int count = (int)min((int64_t)a.blocks, a.total - first);
+  struct Block {
+    int h, t0, n0;
+    bool fresh;  // its rows are not those of the CTA's block before it
+  };
+  auto block = [&](int j) -> Block {
+    const int g = (int)(first + j), pair = g / kOut;
+    return {pair % a.H, pair / a.H * 128, g % kOut * 128, j == 0 || g % kOut == 0};
+  };
   if (tid == 0) {
     prefetch_tensor_map(&tma_x);
     prefetch_tensor_map(&tma_w);
@@ -839,10 +851,11 @@ __global__ void __launch_bounds__(kHeadTcThreads)
       mbar_init(&w_full[i], 1);
       mbar_init(&w_empty[i], 1);
     }
+    mbar_init(&x_full, 1);
+    mbar_init(&x_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&x_full[i], 1);
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], 8);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -857,92 +870,111 @@ __global__ void __launch_bounds__(kHeadTcThreads)
     set_status(a.status, 8);
     return false;
   };
-  const int items = 2 * a.blocks;  // (block, half of K)
   if (w == 0) {
     if (lane == 0) {
-      int issued = 0;
-      for (; issued < items; ++issued) {
-        const int st = issued % L::w_slots, kc = issued & 1, n0 = (nb0 + (issued >> 1)) * 128;
-        if (issued >= L::w_slots && !wait(&w_empty[st], (issued / L::w_slots - 1) & 1)) break;
-        if (issued < 2) {
-          mbar_arrive_expect_tx(&x_full[kc], 128 * 128);
-          tma_load_3d(sm + kc * 128 * 128, &tma_x, 64 * kc, h, t0, &x_full[kc]);
+      int item = 0, xs = 0;  // weight steps and row tiles issued
+      bool ok = true;
+      for (int j = 0; j < count && ok; ++j) {
+        const Block b = block(j);
+        if (b.fresh) {
+          ok = xs == 0 || wait(&x_empty, (xs - 1) & 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&x_full, L::x);
+          tma_load_3d(sm, &tma_x, 0, b.h, b.t0, &x_full);
+          tma_load_3d(sm + L::x / 2, &tma_x, 64, b.h, b.t0, &x_full);
+          ++xs;
         }
-        uint8_t* ws = sm + L::x + st * L::w;
-        mbar_arrive_expect_tx(&w_full[st], L::w);
-        tma_load_2d(ws, &tma_w, n0, h * kLatHead + 64 * kc, &w_full[st]);
-        tma_load_2d(ws + L::w / 2, &tma_w, n0 + 64, h * kLatHead + 64 * kc, &w_full[st]);
+        for (int kc = 0; kc < 2; ++kc, ++item) {
+          const int st = item % L::w_slots;
+          ok = item < L::w_slots || wait(&w_empty[st], (item / L::w_slots - 1) & 1);
+          if (!ok) break;
+          uint8_t* ws = sm + L::x + st * L::w;
+          mbar_arrive_expect_tx(&w_full[st], L::w);
+          tma_load_2d(ws, &tma_w, b.n0, b.h * kLatHead + 64 * kc, &w_full[st]);
+          tma_load_2d(ws + L::w / 2, &tma_w, b.n0 + 64, b.h * kLatHead + 64 * kc, &w_full[st]);
+        }
       }
-      if (issued < items)  // copies in flight land before the CTA ends
-        for (int i = max(0, issued - L::w_slots); i < issued; ++i) mbar_wait(&w_full[i % L::w_slots], (i / L::w_slots) & 1, 100000000ull);
+      if (!ok) {  // copies in flight land before the CTA ends
+        for (int i = max(0, item - L::w_slots); i < item; ++i) mbar_wait(&w_full[i % L::w_slots], (i / L::w_slots) & 1, 100000000ull);
+        if (xs) mbar_wait(&x_full, (xs - 1) & 1, 100000000ull);
+      }
     }
   } else if (w == 1) {
     const uint32_t lead = elect_one();
     constexpr uint32_t id = idesc_bf16(128, 128, false, true);
     bool ok = true;
-    int st = 0, parity = 0;
-    for (int nb = 0; nb < a.blocks && ok; ++nb) {
-      const uint32_t acc = tb + (nb & 1) * 128;
-      if (nb >= 2) ok = __all_sync(0xffffffffu, wait(&acc_empty[nb & 1], ((nb >> 1) - 1) & 1));
+    int st = 0, parity = 0, xs = 0, j = 0;
+    for (; j < count; ++j) {
+      const bool fresh = j == 0 || (first + j) % kOut == 0, leaves = j + 1 == count || (first + j + 1) % kOut == 0;
+      if (fresh) ok = __all_sync(0xffffffffu, wait(&x_full, xs++ & 1));
+      if (ok && j >= 2) ok = __all_sync(0xffffffffu, wait(&acc_empty[j & 1], ((j >> 1) - 1) & 1));
+      const uint32_t acc = tb + (j & 1) * 128;
 #pragma unroll
       for (int kc = 0; kc < 2; ++kc) {
-        ok = ok && __all_sync(0xffffffffu, wait(&x_full[kc], 0) && wait(&w_full[st], parity));
+        ok = ok && __all_sync(0xffffffffu, wait(&w_full[st], parity));
         if (!ok) break;
         fence_after_sync();
-        const uint32_t xs = smem_u32(sm) + kc * 128 * 128, ws = smem_u32(sm) + L::x + st * L::w;
+        const uint32_t x = smem_u32(sm) + kc * (L::x / 2), ws = smem_u32(sm) + L::x + st * L::w;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_bf16_if(lead, acc, sw_desc_k(xs, 128, ks), sw_desc_mn(ws, 64, ks), id, kc || ks ? 1u : 0u);
+          mma_bf16_if(lead, acc, sw_desc_k(x, 128, ks), sw_desc_mn(ws, 64, ks), id, kc || ks ? 1u : 0u);
         commit_if(lead, &w_empty[st]);
         if (++st == L::w_slots) {
           st = 0;
           parity ^= 1;
         }
       }
-      if (ok) commit_if(lead, &acc_full[nb & 1]);
+      if (!ok) break;
+      commit_if(lead, &acc_full[j & 1]);
+      if (leaves) commit_if(lead, &x_empty);
     }
     // the last MMAs are complete before TMEM is freed
-    for (int nb = max(0, a.blocks - 2); nb < a.blocks && ok; ++nb) wait(&acc_full[nb & 1], (nb >> 1) & 1);
+    if (ok && count > 0) wait(&acc_full[(count - 1) & 1], ((count - 1) >> 1) & 1);
     __syncwarp();
   } else {
     const int sp = w & 3;
-    int first = 0, last = a.rows.n_rows;  // rows that belong to a sequence
+    int row0 = 0, row1 = a.rows.n_rows;  // rows that belong to a sequence
     if (a.rows.row_start) {
-      first = a.rows.row_start[0];
-      last = min(last, a.rows.row_start[a.rows.n_seqs]);
+      row0 = a.rows.row_start[0];
+      row1 = min(row1, a.rows.row_start[a.rows.n_seqs]);
     }
-    // this CTA's share of the rotary parts, while the first copies and MMAs run
-    const int64_t r1 = (int64_t)a.rows.n_rows * (blockIdx.x + 1) / gridDim.x;
-    for (int64_t t = (int64_t)a.rows.n_rows * blockIdx.x / gridDim.x + w - 2; t < r1; t += 4)
-      absorb_rope_row(a.rows, a.H, a.q, a.ld_q, a.qa, (int)t);
-    uint8_t* out = sm + L::out + 32 * sp * L::out_ld;  // this warp's rows
-    for (int nb = 0; nb < a.blocks; ++nb) {
-      if (!__all_sync(0xffffffffu, wait(&acc_full[nb & 1], (nb >> 1) & 1))) break;
+    // this CTA's share of the rotary parts: a row per warp and block, while copies and MMAs run
+    int64_t rope = (int64_t)a.rows.n_rows * blockIdx.x / gridDim.x + w - 2;
+    const int64_t rope_end = (int64_t)a.rows.n_rows * (blockIdx.x + 1) / gridDim.x;
+    auto turn = [&] {
+      absorb_rope_row(a.rows, a.rope, a.H, a.q, a.ld_q, a.qa, (int)rope);
+      rope += 8;
+    };
+    // rows 32 sp .. of the tile, one half of a block's columns in steps of 32
+    uint8_t* out = sm + L::out + 32 * (w - 2) * L::out_ld;
+    const int half = 64 * ((w - 2) >> 2);
+    for (int j = 0; j < count; ++j) {
+      if (rope < rope_end) turn();
+      const Block b = block(j);
+      if (!__all_sync(0xffffffffu, wait(&acc_full[j & 1], (j >> 1) & 1))) break;
       fence_after_sync();
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int c0 = half; c0 < half + 64; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32_nowait(tb + ((uint32_t)(32 * sp) << 16) + (j & 1) * 128 + c0, r);
+        tmem_wait_ld();
 #pragma unroll
-        for (int c0 = 0; c0 < 64; c0 += 32) {
-          uint32_t r[32];
-          tmem_ld32_nowait(tb + ((uint32_t)(32 * sp) << 16) + (nb & 1) * 128 + half * 64 + c0, r);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
-          round_to_smem(r, out + lane * L::out_ld + c0 * 2);
-        }
+        for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+        round_to_smem(r, out + lane * L::out_ld);
         __syncwarp();
 #pragma unroll
-        for (int i = lane >> 3; i < 32; i += 4) {
-          const int t = t0 + 32 * sp + i;
-          if (t >= first && t < last)
-            *reinterpret_cast<uint4*>(a.qa + ((size_t)t * a.H + h) * kLatWidth + (nb0 + nb) * 128 + half * 64 + (lane & 7) * 8) =
-                *reinterpret_cast<const uint4*>(out + i * L::out_ld + (lane & 7) * 16);
+        for (int i = lane >> 2; i < 32; i += 8) {
+          const int t = b.t0 + 32 * sp + i;
+          if (t >= row0 && t < row1)
+            *reinterpret_cast<uint4*>(a.qa + ((size_t)t * a.H + b.h) * kLatWidth + b.n0 + c0 + (lane & 3) * 8) =
+                *reinterpret_cast<const uint4*>(out + i * L::out_ld + (lane & 3) * 16);
         }
         __syncwarp();
       }
       fence_before_sync();
-      if (lane == 0) mbar_arrive(&acc_empty[nb & 1]);
+      if (lane == 0) mbar_arrive(&acc_empty[j & 1]);
     }
+    while (rope < rope_end) turn();
   }
   __syncthreads();
   if (w == 1) tmem_dealloc(tb, 256);
@@ -952,6 +984,7 @@ __global__ void __launch_bounds__(kHeadTcThreads)
 // and head.  Bound by reading o.  K steps of 64 through three stages (both operands K-major), M = 128
 // MMAs, the outputs written in whole 256-byte row pieces through the stages' memory.  Two CTAs share an SM
 // and hide one another's epilogue (2047 rows of 32 heads: 14.8 us, 5.94 TB/s).
+constexpr int kExpandThreads = 192;
 struct ExpandSmem {
   static constexpr int stages = 3, steps = kLatDim / 64;
   static constexpr uint32_t half = 128 * 128, stage = 2 * half, out_ld = kLatHead * 2 + 16;
@@ -965,7 +998,7 @@ struct ExpandArgs {
   int* status;
 };
 
-__global__ void __launch_bounds__(kHeadTcThreads)
+__global__ void __launch_bounds__(kExpandThreads)
     latent_expand_tc(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, ExpandArgs a) {
   using namespace tc;
   using L = ExpandSmem;
