@@ -3,7 +3,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cmath>
 #include <string>
 
 #include "../../include/tpc.h"
@@ -25,15 +24,6 @@ static_assert(TPC_LATENT_DIM == tpc::kLatDim && TPC_LATENT_ROPE == tpc::kLatRope
               "cache layout");
 
 constexpr int kLatMaxH = 128;
-
-const tpc::RopeTurns& rope_turns() {
-  static const tpc::RopeTurns r = [] {
-    tpc::RopeTurns x;
-    for (int i = 0; i < tpc::kLatRope / 2; ++i) x.t[i] = std::pow(10000.0, -2.0 * i / tpc::kLatRope) / (2 * M_PI);
-    return x;
-  }();
-  return r;
-}
 
 bool misaligned(const void* p, size_t to = 16) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 
@@ -122,7 +112,7 @@ int tpc_latent_append(const tpc_latent_cache* cache, const tpc_rows* rows, const
     return fail(TPC_ERR_BAD_SHAPE, "latent append: rows of 512 and 64 elements, 16-byte aligned, leading dimensions multiples of 16 bytes");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   tpc_abi::NvtxRange nvtx_call("tpc_latent_append");
-  const tpc::AppendArgs a{lc, r, c, kr, ld_c, ld_kr, status, rope_turns()};
+  const tpc::AppendArgs a{lc, r, c, kr, ld_c, ld_kr, status};
   constexpr int per = tpc::kAppendThreads / 32;
   const unsigned grid = (unsigned)(((int64_t)r.n_rows + per - 1) / per);
   if (in_dtype == TPC_BF16) {
@@ -151,7 +141,7 @@ int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld
   const int64_t total = (int64_t)((r.n_rows + 127) / 128) * H * (tpc::kLatDim / 128);
   const int64_t slots = (int64_t)tpc::kAbsorbPerSm * tpc_abi::sm_count(), blocks = (total + slots - 1) / slots;
   const int64_t grid = (total + blocks - 1) / blocks;
-  const tpc::AbsorbArgs a{r, H, (const bf*)q, ld_q, (bf*)qa, status, total, (int)blocks, rope_turns()};
+  const tpc::AbsorbArgs a{r, H, (const bf*)q, ld_q, (bf*)qa, status, total, (int)blocks};
   constexpr size_t smem = tpc::AbsorbSmem::total;
   TPC_CUDA(set_smem(tpc::latent_absorb_tc, smem));
   TPC_LAUNCH("latent_absorb_tc", st, (tpc::latent_absorb_tc<<<(unsigned)grid, tpc::kAbsorbThreads, smem, st>>>(tx, tw, a)));

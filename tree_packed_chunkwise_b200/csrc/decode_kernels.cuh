@@ -53,11 +53,20 @@ __device__ __forceinline__ RowAt row_at(const DecodeRows& r, int t) {
   return {b, (int64_t)r.kv_len[b] - r.row_start[b + 1] + t};
 }
 
-// 10000^(-2 i / 64) / (2 pi): turns per position of the rotary pair i (computed once on the host; a
-// kernel parameter, so that no thread evaluates a power)
+// 10000^(-2 i / 64) / (2 pi), the turns per position of the rotary pair i, as powers of 10000^(-1 / 32) (their
+// rounding errors stay below i 2^-53 of a value that shrinks by a quarter per i).  A table in memory:
+// lane i's load takes the time of the others beside it, a power in double precision more.
 struct RopeTurns {
   double t[kLatRope / 2];
+  constexpr RopeTurns() : t{} {
+    double x = 0.15915494309189535;
+    for (int i = 0; i < kLatRope / 2; ++i) {
+      t[i] = x;
+      x *= 0.7498942093324559;
+    }
+  }
 };
+__device__ const RopeTurns kRopeTurns{};
 
 // cos and sin of the angle at position pos.  The angle is taken in turns in double precision and reduced
 // there (2^31 positions: error below 1e-6 of a turn), so that far positions keep fp32 accuracy.
@@ -220,7 +229,6 @@ struct AppendArgs {
   const void *c, *kr;
   int64_t ld_c, ld_kr;
   int* status;
-  RopeTurns rope;
 };
 
 constexpr int kAppendThreads = 128;
@@ -228,42 +236,42 @@ constexpr int kAppendThreads = 128;
 // One warp per row: 16 latent elements per lane, then lane i turns the pair (i, i + 32) of the
 // rotary key.  Bound by the row's bytes; each is read and written once.
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t t64 = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   if (t64 >= a.rows.n_rows) return;
   const int t = (int)t64;
+  const T* c = (const T*)a.c + (size_t)t * a.ld_c;
+  const T* kr = (const T*)a.kr + (size_t)t * a.ld_kr;
+  float l[2][8];  // loaded before the search for the row's place, which is a chain of loads itself
+  load_vec<T, 8>(c + lane * 8, l[0]);
+  load_vec<T, 8>(c + (32 + lane) * 8, l[1]);
+  const float x = to_f(kr[lane]), y = to_f(kr[lane + 32]);
   const RowAt r = row_at(a.rows, t);
   if (r.seq < 0 || r.pos < 0) return;
-  const int64_t pg = r.pos / a.cache.page_size;
+  const int pos = (int)r.pos, ps = a.cache.page_size, pg = pos / ps;
   const int page = pg < a.cache.max_pages ? a.cache.table[(size_t)r.seq * a.cache.max_pages + pg] : -1;
   if (page < 0 || page >= a.cache.n_pages) {
     if (lane == 0) set_status(a.status, kStatusCheck);
     return;
   }
-  __nv_bfloat16* dst =
-      a.cache.data + ((size_t)page * a.cache.page_size + (size_t)(r.pos - pg * a.cache.page_size)) * kLatWidth;
-  const T* c = (const T*)a.c + (size_t)t * a.ld_c;
-  const T* kr = (const T*)a.kr + (size_t)t * a.ld_kr;
+  __nv_bfloat16* dst = a.cache.data + ((size_t)page * ps + (pos - pg * ps)) * kLatWidth;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    float x[8];
-    load_vec<T, 8>(c + (j * 32 + lane) * 8, x);
     __align__(16) __nv_bfloat16 e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = __float2bfloat16_rn(x[i]);
+    for (int i = 0; i < 8; ++i) e[i] = __float2bfloat16_rn(l[j][i]);
     reinterpret_cast<uint4*>(dst)[j * 32 + lane] = *reinterpret_cast<const uint4*>(e);
   }
-  const float x = to_f(kr[lane]), y = to_f(kr[lane + 32]);
   float cs, sn;
-  rope_angle(r.pos, a.rope.t[lane], &cs, &sn);
+  rope_angle(pos, kRopeTurns.t[lane], &cs, &sn);
   dst[kLatDim + lane] = __float2bfloat16_rn(x * cs - y * sn);
   dst[kLatDim + 32 + lane] = __float2bfloat16_rn(x * sn + y * cs);
   // a page that two sequences both write: the first row of this run in the page compares it with the
   // pages that its own and later sequences write after it, a sequence per lane
   if (!a.status) return;
-  const int first = a.rows.row_start ? a.rows.row_start[r.seq] : t, ps = a.cache.page_size;
-  if (t != first && r.pos % ps) return;
+  const int first = a.rows.row_start ? a.rows.row_start[r.seq] : t;
+  if (t != first && pos % ps) return;
   bool clash = false;
   if (!a.rows.row_start) {
 #pragma unroll 4
@@ -276,7 +284,7 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __g
       const int64_t m = (int64_t)a.rows.row_start[s + 1] - a.rows.row_start[s];
       const int kv = min(max(a.rows.kv_len[s], 0), a.cache.max_pages * ps), p1 = (kv + ps - 1) / ps;
       if (m <= 0) continue;
-      for (int p = s == r.seq ? (int)pg + 1 : (int)(max((int64_t)0, kv - m) / ps); p < p1; ++p)
+      for (int p = s == r.seq ? pg + 1 : (int)(max((int64_t)0, kv - m) / ps); p < p1; ++p)
         clash |= a.cache.table[(size_t)s * a.cache.max_pages + p] == page;
     }
   }
@@ -286,7 +294,7 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const __g
 // ------------------------------------------------------------------------------------ rotated queries
 // The rotary part of the absorbed queries: a warp turns every head of one row.  Lane i takes cos and sin of
 // angle i; then four lanes hold a head (8 neighbouring pairs each), eight heads at a time.
-__device__ __forceinline__ void absorb_rope_row(const DecodeRows& rows, const RopeTurns& rope, int H,
+__device__ __forceinline__ void absorb_rope_row(const DecodeRows& rows, int H,
                                                 const __nv_bfloat16* q, int64_t ld_q, __nv_bfloat16* qa, int t) {
   const int lane = threadIdx.x & 31, j0 = (lane & 3) * 8;
   const __nv_bfloat16* src = q + (size_t)t * ld_q + kLatHead + j0;
@@ -301,7 +309,7 @@ __device__ __forceinline__ void absorb_rope_row(const DecodeRows& rows, const Ro
   const RowAt r = row_at(rows, t);
   if (r.seq < 0) return;
   float cs, sn, c[8], s[8];
-  rope_angle(r.pos, rope.t[lane], &cs, &sn);
+  rope_angle(r.pos, kRopeTurns.t[lane], &cs, &sn);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     c[j] = __shfl_sync(0xffffffffu, cs, j0 + j);

@@ -820,12 +820,10 @@ struct AbsorbArgs {
   int* status;
   int64_t total;  // blocks in all, and of one CTA
   int blocks;
-  RopeTurns rope;
 };
 
 __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
-    latent_absorb_tc(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w,
-                     const __grid_constant__ AbsorbArgs a) {
+    latent_absorb_tc(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, AbsorbArgs a) {
   using namespace tc;
   using L = AbsorbSmem;
   extern __shared__ __align__(1024) uint8_t hsm_raw[];
@@ -942,7 +940,7 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
     int64_t rope = (int64_t)a.rows.n_rows * blockIdx.x / gridDim.x + w - 2;
     const int64_t rope_end = (int64_t)a.rows.n_rows * (blockIdx.x + 1) / gridDim.x;
     auto turn = [&] {
-      absorb_rope_row(a.rows, a.rope, a.H, a.q, a.ld_q, a.qa, (int)rope);
+      absorb_rope_row(a.rows, a.H, a.q, a.ld_q, a.qa, (int)rope);
       rope += 8;
     };
     // rows 32 sp .. of the tile, one half of a block's columns in steps of 32
