@@ -332,11 +332,11 @@ def test_expand(tpc, n, H):
 
 
 # ------------------------------------------------------------------------------------ attention
-def check_attention(tpc, rng, H, m, kv, page, shared=0, poison=True, extra=0, scale=SCALE, s=1.0, scratch=None):
+def check_attention(tpc, rng, H, m, kv, page, shared=0, poison=True, extra=0, scale=SCALE, s=1.0, scratch=None, table=None):
     import torch
     ragged = extra or any(x != 1 for x in m)
     n = sum(m) + extra
-    table, n_pages = batch(rng, kv, page, shared=shared)
+    table, n_pages = batch(rng, kv, page, shared=shared) if table is None else (table, int(table.max()) + 1)
     cache, c64 = rounded(rng, n_pages, page, 576, dtype=torch.bfloat16)
     if poison:  # whatever lies past the sequences' tokens is never used
         used = np.zeros((n_pages, page), bool)
@@ -579,3 +579,124 @@ def test_wrappers_refuse(tpc):
         with pytest.raises(tpc.TpcError):
             tpc.tpc_latent_expand(o, w)
     assert tpc.tpc_launch_count() == before
+
+
+def test_sampled_branches_match_the_layer_group(tpc):
+    """One KDA and one latent-attention layer of the hybrid group (2048 wide, 16 heads): a prompt, then two branches
+    sampled token by token from its state and its shared pages, against tpc_group_forward over the whole tree.
+    The KDA layer's rows are fp32 on both sides (the group is held to 2e-3 of the RMS, so are its states here).
+    The attention's part of y goes through eight bf16 roundings (q, c, kr, qa, the weights of the softmax, o, the
+    head outputs, and the scores they move), each off by at most half a step: 8 2^-8 of its RMS."""
+    import torch
+    D, H, hd, page, P = 2048, 16, 128, 16, 70
+    branch = [5, 9]
+    g = torch.Generator(device="cuda").manual_seed(40)
+    rnd = lambda *s, scale=1.0: torch.randn(*s, generator=g, device="cuda") * scale
+    W = {"kda": [(rnd(4 * D + H, D, scale=0.02).bfloat16(), rnd(D, D, scale=0.02).bfloat16())],
+         "mla": (rnd(H * 192 + 576, D, scale=0.02).bfloat16(), rnd(2 * D, 512, scale=0.02).bfloat16(), rnd(D, D, scale=0.02).bfloat16())}
+    rows = {0: rnd(P, D), 1: rnd(branch[0], D), 2: rnd(branch[1], D)}
+    tree = tpc.Plan([-1, 0, 0], [P] + branch, 64).upload()
+    at = tree.tables()["row_offset"]
+    x = torch.empty(P + sum(branch), D, device="cuda")
+    for v, r in rows.items():
+        x[at[v]:at[v] + len(r)] = r
+    ws = tpc.group_workspace(tree, 1)
+    y_ref, h_ref = tpc.tpc_group_forward(tree, W, x, ws)
+    assert tpc.tpc_group_status(tree, ws, 1) == 0
+
+    norm = lambda t: t * torch.rsqrt((t * t).mean(-1, keepdim=True) + 1e-6)
+    mul = lambda t, w: t @ w.float().T
+
+    def kda_inputs(t):
+        p = mul(norm(t), W["kda"][0][0])
+        q, k, v, gt = (p[:, i * D:(i + 1) * D].reshape(-1, H, hd) for i in range(4))
+        k = k * torch.rsqrt((k * k).sum(-1, keepdim=True) + 1e-6)
+        return [z.contiguous() for z in (q, k, v, -0.1 * torch.nn.functional.softplus(gt), torch.sigmoid(p[:, 4 * D:]))]
+
+    # the prompt: its KDA state by the chunkwise forward, its latents from the group's KDA output
+    prompt = tpc.Plan([-1], [P], 64).upload()
+    state = torch.zeros(3, H, hd, hd, device="cuda")
+    o, fin, _ = tpc.tpc_kda_forward(prompt, *kda_inputs(rows[0]), split=True)
+    state[0] = fin[0]
+    h0 = h_ref[0][at[0]:at[0] + P]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache = torch.full((16, page, 576), float("nan"), dtype=torch.bfloat16, device="cuda")
+    shared, last = [3, 9, 1, 12], 7  # 64 tokens in full pages, six in a page of their own
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    proj = mul(norm(h0), W["mla"][0])
+    tpc.tpc_latent_append(cache, i32(*shared, last)[None], i32(P), proj[:, H * 192:H * 192 + 512], proj[:, H * 192 + 512:],
+                          row_start=i32(0, P), status=status)
+    cache[4], cache[10] = cache[last], cache[last]  # a branch writes into a copy of the partial page
+    table = torch.stack([i32(*shared, 4), i32(*shared, 10)])
+    scratch = tpc.latent_attn_scratch(H)
+    got_y, got_h, kept = {1: [], 2: []}, {1: [], 2: []}, cache[shared].clone()
+    for t in range(max(branch)):
+        live = [b for b in range(2) if t < branch[b]]
+        xt = torch.stack([rows[1 + b][t] for b in live])
+        dst = i32(*(1 + b for b in live))
+        src = i32(*([0] * len(live))) if t == 0 else dst  # both branches start from the prompt's state
+        o = tpc.tpc_kda_step(state, src, *kda_inputs(xt), dst=dst, status=status)
+        ht = xt + mul(o.reshape(-1, D), W["kda"][0][1])
+        proj = mul(norm(ht), W["mla"][0])
+        kv, tab = i32(*(P + t + 1 for _ in live)), table[live].contiguous()
+        tpc.tpc_latent_append(cache, tab, kv, proj[:, H * 192:H * 192 + 512], proj[:, H * 192 + 512:], status=status)
+        qa = tpc.tpc_latent_absorb(proj[:, :H * 192].bfloat16().view(-1, H, 192), W["mla"][1], kv, status=status)
+        o, _ = tpc.tpc_latent_attn(qa, cache, tab, kv, SCALE, scratch=scratch, status=status)
+        o = tpc.tpc_latent_expand(o, W["mla"][1], status=status)
+        yt = ht + mul(o.float().reshape(-1, D), W["mla"][2])
+        for i, b in enumerate(live):
+            got_h[1 + b].append(ht[i])
+            got_y[1 + b].append(yt[i])
+    assert status.item() == 0 and torch.equal(cache[shared], kept)
+    rms = lambda t: float(t.double().pow(2).mean().sqrt())
+    for v in (1, 2):
+        ref_h, ref_y = (z[at[v]:at[v] + branch[v - 1]] for z in (h_ref[0], y_ref))
+        h, y = torch.stack(got_h[v]), torch.stack(got_y[v])
+        assert float((h - ref_h).abs().max()) <= 4e-3 * rms(ref_h)
+        err = rms((y - h) - (ref_y - ref_h)) / rms(ref_y - ref_h)
+        assert err <= 8 * UBF, err
+
+
+def test_offsets_past_32_bits(tpc):
+    """Caches of more than 2^31 elements: slots and pages at their far end."""
+    import torch
+    rng = np.random.default_rng(41)
+    H, d, slots = 16, 128, 8300  # 2.18e9 fp32 state elements
+    c = step_case(rng, 2, H, d, torch.bfloat16)
+    state = torch.empty(slots, H, d, d, device="cuda")
+    far = np.array([slots - 1, slots - 3], np.int32)
+    state[dev(far).long()] = c["state"][:2]
+    c["src"], small = np.array([0, 1], np.int32), c["state"][:2].clone()
+    args = (c["q"], c["k"], c["v"], c["g"], c["beta"])
+    want = tpc.tpc_kda_step(small, dev(c["src"]), *args)
+    got = tpc.tpc_kda_step(state, dev(far), *args)
+    assert torch.equal(got, want) and torch.equal(state[dev(far).long()], small)
+    del state
+    pages, page = 60000, 64  # 2.2e9 bf16 cache elements
+    cache = torch.empty(pages, page, 576, dtype=torch.bfloat16, device="cuda")
+    near, _ = rounded(rng, 6, page, 576, dtype=torch.bfloat16)
+    order = torch.tensor([pages - 1, pages - 5, 58255, pages - 2, pages - 7, 58254], device="cuda")  # 2^31 / (64 * 576) = 58254.2
+    cache[order] = near
+    kv = dev(np.array([130, 177], np.int32))
+    x, _ = rounded(rng, 2, 576, dtype=torch.bfloat16)
+    qa, _ = rounded(rng, 2, 16, 576, dtype=torch.bfloat16)
+    t_near, t_far = dev(np.arange(6, dtype=np.int32).reshape(2, 3)), order.int().view(2, 3)
+    res = []
+    for ch, tb in ((near, t_near), (cache, t_far)):
+        tpc.tpc_latent_append(ch, tb, kv, x[:, :512], x[:, 512:])
+        res.append(tpc.tpc_latent_attn(qa, ch, tb, kv, SCALE))
+    assert torch.equal(cache[order], near)
+    assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+
+
+def test_attention_of_idle_and_long_sequences(tpc):
+    """Thousands of sequences of which few have a row, and one long context among empty ones."""
+    rng = np.random.default_rng(42)
+    m, kv = [0] * 3000, [0] * 3000
+    table = np.zeros((3000, 63), np.int32)  # idle sequences' entries are page 0
+    for i, (b, (rows, length)) in enumerate({7: (1, 33), 1500: (5, 4000), 2999: (2, 700)}.items()):
+        m[b], kv[b], table[b] = rows, length, 1 + 63 * i + rng.permutation(63)
+    check_attention(tpc, rng, 8, m, kv, 64, poison=False, table=table)
+    table = np.zeros((20, 282), np.int32)
+    table[10] = 1 + rng.permutation(282)
+    check_attention(tpc, rng, 16, [1] * 20, [0] * 10 + [9000] + [0] * 9, 32, poison=False, table=table)
