@@ -46,7 +46,8 @@ def rounded(rng, *shape, dtype, s=1.0):
 
 
 def within(x, ref, tol, what):
-    bad = ~(np.abs(x - ref) <= tol) & ~(x == ref)  # a NaN is bad, equal infinities are not
+    with np.errstate(invalid="ignore"):
+        bad = ~(np.abs(x - ref) <= tol) & ~(x == ref)  # a NaN is bad, equal infinities are not
     i = np.argmax(bad) if bad.size else 0
     assert not bad.any(), (what, int(bad.sum()), np.unravel_index(i, x.shape), x.flat[i], ref.flat[i],
                            np.broadcast_to(tol, x.shape).flat[i])
