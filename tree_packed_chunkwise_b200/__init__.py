@@ -947,7 +947,11 @@ def tpc_kda_step(state, src, q, k, v, g, beta, dst=None, row_start=None, out_dty
     p_dst = 0 if dst is None else _want("dst", dst, i32, (n_seqs,), dev)
     batch = _decode_rows(n, row_start, 0, n_seqs, dev)
     status = _status(status, dev)
-    o, p_o = _out("o", o, q, out_dtype, rows, dev, stream)
+    if o is None and stream is None and out_dtype is dt:
+        o = torch.empty_like(q)  # the cheapest allocation there is
+        p_o = o.data_ptr()
+    else:
+        o, p_o = _out("o", o, q, out_dtype, rows, dev, stream)
     _check(lib().tpc_kda_step(_pack_shape(H, d, d, dt is bf, out_dtype is bf), batch,
                               _pack_step(p_q, p_k, p_v, p_g, p_beta, p_state, n_slots, p_src, p_dst, p_o), status,
                               _decode_stream(stream, dev)))

@@ -981,7 +981,8 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
 // The head outputs out[t][h][i] = sum_l W_v[h][i][l] o[t][h][l] (K = 512, 128 outputs), one CTA per 128 rows
 // and head.  Bound by reading o.  K steps of 64 through three stages (both operands K-major), M = 128
 // MMAs, the outputs written in whole 256-byte row pieces through the stages' memory.  Two CTAs share an SM
-// and hide one another's epilogue (2047 rows of 32 heads: 14.8 us, 5.94 TB/s).
+// and hide one another's epilogue (2047 rows of 32 heads: 14.6 us, 6.0 TB/s, inputs partly in L2; 20.5 us
+// from memory.  Equal shares of consecutive tiles with two accumulators a CTA: 14.3 and 20.7 us).
 constexpr int kExpandThreads = 192;
 struct ExpandSmem {
   static constexpr int stages = 3, steps = kLatDim / 64;
