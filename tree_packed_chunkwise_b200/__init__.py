@@ -850,17 +850,16 @@ def _want(name, t, dtype, shape, dev):
                       f"{tuple(t.shape)} (strides {t.stride()}) on {t.device}")
 
 
-def _want_rows(name, t, dtype, shape, dev):
-    """As _want for a tensor whose rows (dimension 0) may lie further apart: (address, elements from row to row)."""
-    n, inner = t.shape[0] if t.dim() else 0, 1
-    ok = t.dtype is dtype and t.shape == shape and t.get_device() == dev
-    for d in range(len(shape) - 1, 0, -1):
-        ok = ok and (t.stride(d) == inner or t.shape[d] == 1 or n == 0)
-        inner *= shape[d]
-    if not ok:
-        raise TpcError(2, f"{name} must be a {dtype} tensor {shape} with contiguous rows on cuda:{dev}, got {t.dtype} "
-                          f"{tuple(t.shape)} (strides {t.stride()}) on {t.device}")
-    return t.data_ptr(), t.stride(0) if n > 1 else inner  # the stride of a single row says nothing
+def _want_rows(name, t, dtype, shape, inner, dev):
+    """As _want for a tensor whose rows (dimension 0) may lie further apart, with the strides `inner` inside a row:
+    (address, elements from row to row)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        strides = t.stride()
+        # the stride of a dimension of size 1 says nothing
+        if strides[1:] == inner or all(a == b or n == 1 for a, b, n in zip(strides[1:], inner, shape[1:])) or shape[0] == 0:
+            return t.data_ptr(), strides[0] if shape[0] > 1 else shape[1] * inner[0]
+    raise TpcError(2, f"{name} must be a {dtype} tensor {shape} with contiguous rows on cuda:{dev}, got {t.dtype} "
+                      f"{tuple(t.shape)} (strides {t.stride()}) on {t.device}")
 
 
 def _decode_device(t):
@@ -970,8 +969,8 @@ def tpc_latent_append(cache, block_table, kv_len, c, kr, row_start=None, status=
     if c.dim() != 2 or (dt is not torch.bfloat16 and dt is not torch.float32):
         raise TpcError(2, f"c must be bf16 or fp32 [n_rows, {LATENT_DIM}], got {dt} {tuple(c.shape)}")
     n = c.shape[0]
-    p_c, ld_c = _want_rows("c", c, dt, (n, LATENT_DIM), dev)
-    p_kr, ld_kr = _want_rows("kr", kr, dt, (n, LATENT_ROPE), dev)
+    p_c, ld_c = _want_rows("c", c, dt, (n, LATENT_DIM), (1,), dev)
+    p_kr, ld_kr = _want_rows("kr", kr, dt, (n, LATENT_ROPE), (1,), dev)
     batch = _decode_rows(n, row_start, p_kv, n_seqs, dev)
     _check(lib().tpc_latent_append(lc, batch, p_c, ld_c, p_kr, ld_kr, dt is torch.bfloat16, _status(status, dev),
                                    _decode_stream(stream, dev)))
@@ -985,7 +984,7 @@ def tpc_latent_absorb(q, w_b, kv_len, row_start=None, qa=None, status=None, stre
     if q.dim() != 3:
         raise TpcError(2, f"q must be [n_rows, H, {LATENT_HEAD + LATENT_ROPE}], got {tuple(q.shape)}")
     n, H, _ = q.shape
-    p_q, ld_q = _want_rows("q", q, bf, (n, H, LATENT_HEAD + LATENT_ROPE), dev)
+    p_q, ld_q = _want_rows("q", q, bf, (n, H, LATENT_HEAD + LATENT_ROPE), (LATENT_HEAD + LATENT_ROPE, 1), dev)
     p_w = _want("w_b", w_b, bf, (2 * LATENT_HEAD * H, LATENT_DIM), dev)
     batch = _decode_rows(n, row_start, p_kv, n_seqs, dev)
     status = _status(status, dev)
