@@ -69,14 +69,15 @@ struct LatSmem {
 static_assert(LatSmem<64>::total <= 232448 && LatSmem<32>::total <= 232448 && LatSmem<16>::total <= 232448,
               "shared memory of one CTA");
 
-// scratch: partial sums of the pieces (two per CTA), their (max, sum), and one record per CTA
+// scratch: partial sums of the pieces (two per CTA), their (maximum, sum of the weights, sum of the rounded
+// weights), and one record per CTA
 struct LatPiece {
   int col0;  // first (row, head) pair of the split unit that starts in this CTA
   int ncols;
   int n;     // its pieces: this CTA's last one, then the first ones of the next n - 1 CTAs
 };
 constexpr size_t kLatPartBytes = (size_t)kLatMaxCtas * 2 * kLatMaxNT * kLatDim * 4;
-constexpr size_t kLatMlBytes = (size_t)kLatMaxCtas * 2 * kLatMaxNT * 8;
+constexpr size_t kLatMlBytes = (size_t)kLatMaxCtas * 2 * kLatMaxNT * 16;
 constexpr size_t kLatScratch = kLatPartBytes + kLatMlBytes + ((kLatMaxCtas * sizeof(LatPiece) + 255) / 256) * 256;
 
 struct LatAttnArgs {
@@ -87,7 +88,7 @@ struct LatAttnArgs {
   __nv_bfloat16* o;
   float* lse;
   float* part;
-  float2* ml;
+  float4* ml;
   LatPiece* meta;
   int* status;
 };
@@ -492,11 +493,11 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       // last visible position of every column (columns past the run's end take its last row's)
       if (st < NT) lim[st] = s.kv - s.m + min((walk.ct * NT + st) / a.H, s.m - 1);
       const int lim0 = s.kv - s.m + walk.ct * NT / a.H;
-      float mx[2 * R], sum[2 * R];
+      float mx[2 * R], sum[2 * R], sumr[2 * R];
 #pragma unroll
       for (int c = 0; c < 2 * R; ++c) {
         mx[c] = -INFINITY;
-        sum[c] = 0.f;
+        sum[c] = sumr[c] = 0.f;
       }
       meet();  // lim is set; the last piece's reads of red and fac are over
       for (int i = 0; i < walk.n; ++i, ++it) {
@@ -553,6 +554,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
             const float f = m2 == -INFINITY ? 1.f : ex2(mx[c] - m2);
             mx[c] = m2;
             sum[c] *= f;
+            sumr[c] *= f;
             tm[c] = f;
           }
         }
@@ -577,8 +579,9 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
             }
           }
         }
-        // weights: fp32 into the sums, bf16 into the product (the tensor core's operand type; the
-        // rounding errors are independent and average over the row)
+        // weights: fp32 into the sum of the log-sum-exp, bf16 into the product (the tensor core's operand
+        // type).  The product is divided by the sum of the rounded weights, so that what is summed has weights
+        // of sum 1: a row that one token dominates is as exact as that token.
 #pragma unroll
         for (int c = 0; c < 2 * R; ++c) {
           const float m = mx[c] == -INFINITY ? 0.f : mx[c];
@@ -595,9 +598,14 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
 #pragma unroll
           for (int j = 0; j < R; j += 2) {
             const int n = 8 * (j + (lane >> 4)) + (lane & 7), unit = 4 * (sp & 1) + 2 * g + ((lane >> 3) & 1);
-            stmatrix4_trans(ph + n * 128 + ((unit ^ (lane & 7)) << 4), pack_bf16(x[g][4 * j], x[g][4 * j + 1]),
-                            pack_bf16(x[g][4 * j + 2], x[g][4 * j + 3]), pack_bf16(x[g][4 * j + 4], x[g][4 * j + 5]),
-                            pack_bf16(x[g][4 * j + 6], x[g][4 * j + 7]));
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              p[e] = pack_bf16(x[g][4 * j + 2 * e], x[g][4 * j + 2 * e + 1]);
+              sumr[2 * j + (e & 2)] += __uint_as_float(p[e] << 16);
+              sumr[2 * j + (e & 2) + 1] += __uint_as_float(p[e] & 0xffff0000u);
+            }
+            stmatrix4_trans(ph + n * 128 + ((unit ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
           }
         // rows of the tile that hold no token of the sequence: their weights are 0, but whatever the
         // page holds there (NaN among it) must not meet them
@@ -617,34 +625,42 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       // ---- end of the piece: sums over the tokens, then O^T out of tensor memory
 #pragma unroll
       for (int c = 0; c < 2 * R; ++c) {
-        sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 4);
-        sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 8);
-        sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 16);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], d);
+          sumr[c] += __shfl_xor_sync(0xffffffffu, sumr[c], d);
+        }
       }
       meet();  // red and fac have been read
       if (lane < 4) {
 #pragma unroll
         for (int j = 0; j < R; ++j) {
           *reinterpret_cast<float2*>(red + sp * NT + 8 * j + 2 * lane) = make_float2(sum[2 * j], sum[2 * j + 1]);
+          *reinterpret_cast<float2*>(red + (4 + sp) * NT + 8 * j + 2 * lane) = make_float2(sumr[2 * j], sumr[2 * j + 1]);
           if (sp == 0) *reinterpret_cast<float2*>(fac + 8 * j + 2 * lane) = make_float2(mx[2 * j], mx[2 * j + 1]);
         }
       }
       meet();
       const bool whole = walk.t0 == 0 && walk.n == walk.tiles;
       const int slot = 2 * blockIdx.x + (walk.t0 == 0 ? 1 : 0);
-      const float l = st < NT ? red[st] + red[NT + st] + red[2 * NT + st] + red[3 * NT + st] : 0.f;
+      float l = 0.f, lr = 0.f;
+      if (st < NT)
+        for (int i = 0; i < 4; ++i) {
+          l += red[i * NT + st];
+          lr += red[(4 + i) * NT + st];
+        }
       if (st < ncols) {
         if (whole)
           a.lse[col0 + st] = l == 0.f ? -INFINITY : (fac[st] + log2f(l)) * 0.6931471805599453f;
         else
-          a.ml[slot * kLatMaxNT + st] = make_float2(fac[st], l);
+          a.ml[slot * kLatMaxNT + st] = make_float4(fac[st], l, lr, 0.f);
       }
       if (!whole && walk.t0 == 0 && st == 0) {
         const long long rest = walk.tiles - walk.n;
         a.meta[blockIdx.x] = {col0, ncols, 1 + (int)((rest + per - 1) / per)};
       }
       meet();
-      if (st < NT) fac[st] = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      if (st < NT) fac[st] = !whole ? 1.f : lr == 0.f ? 0.f : 1.f / lr;
       meet();
       wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
       __syncwarp();
@@ -673,7 +689,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
 }
 
 // Joins the pieces of every unit that starts in one share and ends in a later one:
-//   o = sum_i e^{m_i - m} O_i / sum_i e^{m_i - m} l_i,
+//   o = sum_i e^{m_i - m} O_i / sum_i e^{m_i - m} r_i  (r: sums of the rounded weights; lse from the others),
 // in an order that depends on the number of pieces alone.  Launched while the attention kernel still
 // runs (it waits for that grid's end).  Its time is that of a chain of loads, so a thread takes at most
 // 4 to 10 pieces, mostly loaded at once, and the CTAs share a list of work items of three kinds:
@@ -693,8 +709,8 @@ struct LatJoin {  // running sum of pieces for 4 dimensions of a column
     o.z = fmaf(e, x.z, o.z);
     o.w = fmaf(e, x.w, o.w);
   }
-  __device__ __forceinline__ void store(const LatAttnArgs& a, size_t col, int d, float m, float l) const {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+  __device__ __forceinline__ void store(const LatAttnArgs& a, size_t col, int d, float m, float l, float r) const {
+    const float inv = r == 0.f ? 0.f : 1.f / r;
     const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     store4(a.o + col * kLatDim + d, v);
     if (d == 0) a.lse[col] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -737,8 +753,8 @@ __global__ void __launch_bounds__(kLatCombThreads, 2) latent_combine_kernel(LatA
     if (u.n <= kLatCombFew) {
       const int c = 4 * k + (tid >> 7), d = 4 * (tid & 127);
       if (c >= u.ncols) continue;
-      float m = -INFINITY, l = 0.f;
-      float2 ml[kLatCombFew];
+      float m = -INFINITY, l = 0.f, r = 0.f;
+      float4 ml[kLatCombFew];
       float4 x[kLatCombFew];
 #pragma unroll
       for (int i = 0; i < kLatCombFew; ++i)
@@ -753,28 +769,33 @@ __global__ void __launch_bounds__(kLatCombThreads, 2) latent_combine_kernel(LatA
         if (i < u.n) {
           const float e = tc::ex2(ml[i].x - m);
           l = fmaf(e, ml[i].y, l);
+          r = fmaf(e, ml[i].z, r);
           join.add(e, x[i]);
         }
-      join.store(a, (size_t)u.col0 + c, d, m, l);
+      join.store(a, (size_t)u.col0 + c, d, m, l, r);
       continue;
     }
     // G groups of threads, group g takes pieces g, g + G, ...; d: the thread's dimensions
     const bool some = u.n <= kLatCombSome;
     const int c = some ? k : k >> 2, d = some ? 4 * (tid & 127) : 128 * (k & 3) + 4 * lane;
     const int G = some ? kLatCombThreads / 128 : kLatCombThreads / 32, g = some ? tid >> 7 : w;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, r = 0.f;
     for (int i = lane; i < u.n; i += 32) m = fmaxf(m, a.ml[slot(i) + c].x);
 #pragma unroll
     for (int e = 16; e; e >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
     if (m == -INFINITY) m = 0.f;
     for (int i = lane; i < u.n; i += 32) {
-      const float2 ml = a.ml[slot(i) + c];
+      const float4 ml = a.ml[slot(i) + c];
       const float e = tc::ex2(ml.x - m);
       if (w == 0) f[i] = e;
       l = fmaf(e, ml.y, l);
+      r = fmaf(e, ml.z, r);
     }
 #pragma unroll
-    for (int e = 16; e; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
+    for (int e = 16; e; e >>= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, e);
+      r += __shfl_xor_sync(0xffffffffu, r, e);
+    }
     __syncthreads();
 #pragma unroll 5
     for (int i = g; i < u.n; i += G)
@@ -785,7 +806,7 @@ __global__ void __launch_bounds__(kLatCombThreads, 2) latent_combine_kernel(LatA
       const int step = kLatCombThreads / G;
 #pragma unroll 3
       for (int i = 1; i < G; ++i) join.add(1.f, acc_s[step * i + tid]);
-      join.store(a, (size_t)u.col0 + c, d, m, l);
+      join.store(a, (size_t)u.col0 + c, d, m, l, r);
     }
     __syncthreads();  // f and acc_s are free again
   }
