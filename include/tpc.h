@@ -557,7 +557,7 @@ typedef struct tpc_rows {
  *   rows hold unspecified values (the comparison of every sequence with every other one adds
  *   1 us at 100 sequences, 5 us at 4096).
  *   shape: dk == dv in {32, 64, 128}, H >= 1, in_dtype TPC_F32 or TPC_BF16 (q, k, v, g, beta).
- *   q, k, v, g: [n_rows, H, d], beta [n_rows, H], 16-byte aligned.  g may be any value <= 0,
+ *   q, k, v, g: [n_rows, H, d], beta [n_rows, H], 16-byte aligned; o overlaps none of them.  g may be any value <= 0,
  *   -infinity included (the channel's state is dropped).
  * Errors: TPC_ERR_NULL, TPC_ERR_BAD_SHAPE, TPC_ERR_UNSUPPORTED, TPC_ERR_CUDA.
  */
@@ -625,7 +625,8 @@ int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld
  * weights enter their product as bf16 and are normalised as such.  qa: [n_rows][H][576] bf16,
  * 16-byte aligned, 1 <= H <= 128.
  *   scratch: tpc_latent_attn_scratch_bytes(H) bytes, 256-byte aligned, used by one call at a time.
- * Deterministic: the same call gives the same bits.  A block table entry outside 0 .. n_pages - 1
+ * Deterministic: the same call gives the same bits (the pieces that a long context is summed in depend
+ * on the whole batch, so another batch may round a sequence differently).  A block table entry outside 0 .. n_pages - 1
  * or a kv_len beyond max_pages * page_size records TPC_ERR_DEVICE_CHECK (the sequence's rows are
  * then unspecified).
  */

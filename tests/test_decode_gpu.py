@@ -447,6 +447,39 @@ def test_attention_bad_tables(tpc):
     assert status.item() == 0
 
 
+def test_bad_row_starts(tpc):
+    """Row tables that decrease or leave the rows: reported by the step and the attention, followed by no call
+    (what lies around the tensors keeps its values)."""
+    import torch
+    rng = np.random.default_rng(24)
+    H, big = 2, 2 ** 31 - 1
+    i32 = lambda a: dev(np.array(a, np.int32))
+    for start in ([0, 2, 1, 3], [-4, 1, 2, 3], [0, 1, 2, 9], [big, 0, 1, 3], [0, -big, big, 3], [3, 2, 1, 0]):
+        guard = torch.full((9, H, 576), -7.0, dtype=torch.bfloat16, device="cuda")
+        qa, w_b, cache = (rounded(rng, *s, dtype=torch.bfloat16)[0] for s in ((3, H, 576), (512, 512), (6, 16, 576)))
+        table, kv = i32(rng.permutation(6).reshape(3, 2)), i32([20, 5, big])
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        qo = guard.clone()
+        tpc.tpc_latent_absorb(qa[:, :, :192].contiguous(), w_b, kv, row_start=i32(start), qa=qo[3:6], status=status)
+        c, kr = rounded(rng, 3, 512, dtype=torch.bfloat16)[0], rounded(rng, 3, 64, dtype=torch.bfloat16)[0]
+        pool = guard.new_full((18, 16, 576), -7.0)
+        tpc.tpc_latent_append(pool[6:12], table, kv, c, kr, row_start=i32(start), status=status)
+        ao, al = guard.new_full((9, H, 512), -7.0), torch.full((9, H), -7.0, device="cuda")
+        status.zero_()
+        tpc.tpc_latent_attn(qa, cache, table, kv, SCALE, row_start=i32(start), o=ao[3:6], lse=al[3:6], status=status)
+        assert status.item() == 7, start
+        for t in (qo, ao, al):
+            assert bool((t[:3] == -7).all()) and bool((t[6:] == -7).all()), start
+        assert bool((pool[:6] == -7).all()) and bool((pool[12:] == -7).all()), start
+        x, st = rounded(rng, 3, H, 64, dtype=torch.float32)[0], rounded(rng, 9, H, 64, 64, dtype=torch.float32)[0]
+        keep, so = st.clone(), torch.full((9, H, 64), -7.0, device="cuda")
+        status.zero_()
+        tpc.tpc_kda_step(st[3:6], i32([0, 1, 2]), x, x, x, -x.abs(), x[:, :, 0].contiguous(), row_start=i32(start), o=so[3:6], status=status)
+        assert status.item() == 7, start
+        assert torch.equal(st[:3], keep[:3]) and torch.equal(st[6:], keep[6:])
+        assert bool((so[:3] == -7).all()) and bool((so[6:] == -7).all()), start
+
+
 # ------------------------------------------------------------------------------------ together
 def test_generation_matches_the_expanded_attention(tpc):
     """A prompt and then single tokens through append, absorb, attention and expand equal the expanded causal

@@ -249,8 +249,10 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendArg
   const float x = to_f(kr[lane]), y = to_f(kr[lane + 32]);
   const RowAt r = row_at(a.rows, t);
   if (r.seq < 0 || r.pos < 0) return;
-  const int pos = (int)r.pos, ps = a.cache.page_size, pg = pos / ps;
-  const int page = pg < a.cache.max_pages ? a.cache.table[(size_t)r.seq * a.cache.max_pages + pg] : -1;
+  const int ps = a.cache.page_size;
+  const bool fits = r.pos < (int64_t)a.cache.max_pages * ps;
+  const int pos = fits ? (int)r.pos : 0, pg = pos / ps;
+  const int page = fits ? a.cache.table[(size_t)r.seq * a.cache.max_pages + pg] : -1;
   if (page < 0 || page >= a.cache.n_pages) {
     if (lane == 0) set_status(a.status, kStatusCheck);
     return;
