@@ -165,7 +165,7 @@ int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   tpc_abi::NvtxRange nvtx_call("tpc_latent_attn");
   CUtensorMap tkv, tq;
-  // columns of a tile: the (row, head) pairs that an average sequence has
+  // columns of a tile: the (row, head) pairs that an average sequence has (times at the kernel)
   const int64_t cols = ((int64_t)r.n_rows * H + r.n_seqs - 1) / r.n_seqs;
   const int NT = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
   if (!tensor_map(&tkv, lc.data, tpc::kLatWidth, (uint64_t)lc.n_pages * lc.page_size, tpc::kLatWidth, std::min(lc.page_size, tpc::kLatBox)) ||
@@ -206,16 +206,23 @@ int tpc_latent_expand(int32_t n_rows, int32_t H, const void* o, const void* w_b,
   if (misaligned(o) || misaligned(w_b) || misaligned(out)) return fail(TPC_ERR_BAD_SHAPE, "latent expand: tensors must be 16-byte aligned");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   tpc_abi::NvtxRange nvtx_call("tpc_latent_expand");
-  CUtensorMap tx, tw;
-  if (!tensor_map_rows(&tx, o, tpc::kLatDim, H, n_rows, 128) ||
-      !tensor_map(&tw, w_b, tpc::kLatDim, (uint64_t)2 * tpc::kLatHead * H, tpc::kLatDim, 128))
-    return fail(TPC_ERR_CUDA, "latent expand: cuTensorMapEncodeTiled failed");
   const tpc::ExpandArgs a{H, n_rows, (bf*)out, status};
-  const unsigned grid = (unsigned)((int64_t)((n_rows + 127) / 128) * H);
-  constexpr size_t smem = tpc::ExpandSmem::total;
-  TPC_CUDA(set_smem(tpc::latent_expand_tc, smem));
-  TPC_LAUNCH("latent_expand_tc", st, (tpc::latent_expand_tc<<<grid, tpc::kExpandThreads, smem, st>>>(tx, tw, a)));
-  return TPC_OK;
+  const int64_t pairs = (int64_t)((n_rows + 127) / 128) * H;
+  auto go = [&](auto bn) -> int {
+    constexpr int BN = decltype(bn)::value;
+    CUtensorMap tx, tw;
+    if (!tensor_map_rows(&tx, o, tpc::kLatDim, H, n_rows, 128) ||
+        !tensor_map(&tw, w_b, tpc::kLatDim, (uint64_t)2 * tpc::kLatHead * H, tpc::kLatDim, BN))
+      return fail(TPC_ERR_CUDA, "latent expand: cuTensorMapEncodeTiled failed");
+    const unsigned grid = (unsigned)(pairs * (tpc::kLatHead / BN));
+    constexpr size_t smem = tpc::ExpandSmem<BN>::total;
+    TPC_CUDA(set_smem(tpc::latent_expand_tc<BN>, smem));
+    TPC_LAUNCH("latent_expand_tc", st, (tpc::latent_expand_tc<BN><<<grid, tpc::kExpandThreads, smem, st>>>(tx, tw, a)));
+    return TPC_OK;
+  };
+  // narrow output blocks while their CTAs fit the SMs twice (both sides at the kernel)
+  if (pairs * (tpc::kLatHead / 32) <= 2 * tpc_abi::sm_count()) return go(std::integral_constant<int, 32>{});
+  return go(std::integral_constant<int, 128>{});
 }
 
 }  // extern "C"

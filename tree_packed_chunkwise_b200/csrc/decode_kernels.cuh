@@ -99,14 +99,9 @@ __device__ __forceinline__ void load_vec(const T* p, float (&x)[N]) {
 #pragma unroll
       for (int i = 0; i < V; ++i) x[j * V + i] = to_f(e[i]);
     }
-  } else if constexpr (B == 8) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = to_f(e[i]);
   } else {
-    static_assert(B == 4, "vector width");
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    static_assert(B == 8, "vector width");
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
     const T* e = reinterpret_cast<const T*>(&u);
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = to_f(e[i]);

@@ -1006,15 +1006,18 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
   if (w == 1) tmem_dealloc(tb, 256);
 }
 
-// The head outputs out[t][h][i] = sum_l W_v[h][i][l] o[t][h][l] (K = 512, 128 outputs), one CTA per 128 rows
-// and head.  Bound by reading o.  K steps of 64 through three stages (both operands K-major), M = 128
-// MMAs, the outputs written in whole 256-byte row pieces through the stages' memory.  Two CTAs share an SM
+// The head outputs out[t][h][i] = sum_l W_v[h][i][l] o[t][h][l] (K = 512, 128 outputs), one CTA per 128 rows,
+// head and BN outputs.  Bound by reading o.  K steps of 64 through three stages (both operands K-major),
+// M = 128 MMAs, the outputs written in whole row pieces through the stages' memory.  Two CTAs share an SM
 // and hide one another's epilogue (2047 rows of 32 heads: 14.6 us, 6.0 TB/s, inputs partly in L2; 20.5 us
-// from memory.  Equal shares of consecutive tiles with two accumulators a CTA: 14.3 and 20.7 us).
+// from memory.  Equal shares of consecutive tiles with two accumulators a CTA: 14.3 and 20.7 us).  A few
+// rows are a chain of fetching a head's weights, which BN = 32 cuts to a quarter (96
+// rows of 16 heads 4.2 against 5.3 us, 500 rows 5.5 against 5.6; 96 rows of 128 heads 8.5 against 5.6 us).
 constexpr int kExpandThreads = 192;
+template <int BN>
 struct ExpandSmem {
   static constexpr int stages = 3, steps = kLatDim / 64;
-  static constexpr uint32_t half = 128 * 128, stage = 2 * half, out_ld = kLatHead * 2 + 16;
+  static constexpr uint32_t x = 128 * 128, stage = x + BN * 128, out_ld = BN * 2 + 16;
   static constexpr uint32_t total = stages * stage + 1024;  // + slack to align the stages
   static_assert(128 * out_ld <= stages * stage, "the output tile takes the stages' place");
 };
@@ -1025,16 +1028,18 @@ struct ExpandArgs {
   int* status;
 };
 
+template <int BN>
 __global__ void __launch_bounds__(kExpandThreads)
     latent_expand_tc(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w, ExpandArgs a) {
   using namespace tc;
-  using L = ExpandSmem;
+  using L = ExpandSmem<BN>;
   extern __shared__ __align__(1024) uint8_t hsm_raw[];
   uint8_t* sm = hsm_raw + ((1024u - (smem_u32(hsm_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t full[L::stages], empty[L::stages], acc_full;
   __shared__ uint32_t tslot;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  const int h = (int)(blockIdx.x % a.H), t0 = (int)(blockIdx.x / a.H) * 128;
+  const int n0 = (int)(blockIdx.x % (kLatHead / BN)) * BN, pair = (int)(blockIdx.x / (kLatHead / BN));
+  const int h = pair % a.H, t0 = pair / a.H * 128;
   if (tid == 0) {
     prefetch_tensor_map(&tma_x);
     prefetch_tensor_map(&tma_w);
@@ -1045,7 +1050,7 @@ __global__ void __launch_bounds__(kExpandThreads)
     mbar_init(&acc_full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (w == 1) tmem_alloc(&tslot, 128);
+  if (w == 1) tmem_alloc(&tslot, BN);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -1065,14 +1070,14 @@ __global__ void __launch_bounds__(kExpandThreads)
         uint8_t* xs = sm + st * L::stage;
         mbar_arrive_expect_tx(&full[st], L::stage);
         tma_load_3d(xs, &tma_x, k0, h, t0, &full[st]);
-        tma_load_2d(xs + L::half, &tma_w, k0, (a.H + h) * kLatHead, &full[st]);
+        tma_load_2d(xs + L::x, &tma_w, k0, (a.H + h) * kLatHead + n0, &full[st]);
       }
       if (issued < L::steps)  // copies in flight land before the CTA ends
         for (int i = max(0, issued - L::stages); i < issued; ++i) mbar_wait(&full[i % L::stages], (i / L::stages) & 1, 100000000ull);
     }
   } else if (w == 1) {
     const uint32_t lead = elect_one();
-    constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+    constexpr uint32_t id = idesc_bf16(128, BN, false, false);
     bool ok = true;
 #pragma unroll
     for (int i = 0; i < L::steps; ++i) {
@@ -1082,7 +1087,7 @@ __global__ void __launch_bounds__(kExpandThreads)
       fence_after_sync();
       const uint32_t xs = smem_u32(sm) + st * L::stage;
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) mma_bf16_if(lead, tb, sw_desc_k(xs, 128, ks), sw_desc_k(xs + L::half, 128, ks), id, i || ks ? 1u : 0u);
+      for (int ks = 0; ks < 4; ++ks) mma_bf16_if(lead, tb, sw_desc_k(xs, 128, ks), sw_desc_k(xs + L::x, BN, ks), id, i || ks ? 1u : 0u);
       commit_if(lead, &empty[st]);
     }
     // also after a wait that ran out: the MMAs issued so far are complete before TMEM is freed, but then
@@ -1097,7 +1102,7 @@ __global__ void __launch_bounds__(kExpandThreads)
     uint8_t* out = sm + 32 * sp * L::out_ld;  // this warp's rows; every copy has landed and been read
     if (got) {
 #pragma unroll
-      for (int c0 = 0; c0 < kLatHead; c0 += 32) {
+      for (int c0 = 0; c0 < BN; c0 += 32) {
         uint32_t r[32];
         tmem_ld32_nowait(tb + ((uint32_t)(32 * sp) << 16) + c0, r);
         tmem_wait_ld();
@@ -1106,18 +1111,19 @@ __global__ void __launch_bounds__(kExpandThreads)
         round_to_smem(r, out + lane * L::out_ld + c0 * 2);
       }
       __syncwarp();
+      constexpr int lanes = BN / 8;  // of a row piece
 #pragma unroll 4
-      for (int i = lane >> 4; i < 32; i += 2) {
+      for (int i = lane / lanes; i < 32; i += 32 / lanes) {
         const int t = t0 + 32 * sp + i;
         if (t < a.n_rows)
-          *reinterpret_cast<uint4*>(a.out + ((size_t)t * a.H + h) * kLatHead + (lane & 15) * 8) =
-              *reinterpret_cast<const uint4*>(out + i * L::out_ld + (lane & 15) * 16);
+          *reinterpret_cast<uint4*>(a.out + ((size_t)t * a.H + h) * kLatHead + n0 + lane % lanes * 8) =
+              *reinterpret_cast<const uint4*>(out + i * L::out_ld + lane % lanes * 16);
       }
     }
     fence_before_sync();
   }
   __syncthreads();
-  if (w == 1) tmem_dealloc(tb, 128);
+  if (w == 1) tmem_dealloc(tb, BN);
 }
 
 }  // namespace tpc
