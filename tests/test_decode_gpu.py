@@ -403,6 +403,16 @@ def test_attention_batches(tpc):
     check_attention(tpc, rng, 16, [int(x) for x in rng.integers(0, 5, 150)], [int(x) for x in rng.integers(5, 600, 150)], 16)
 
 
+def test_attention_of_short_tables(tpc):
+    """Tables of at most 128 tokens (one tile a context, no joining) and just above, many and few sequences."""
+    rng = np.random.default_rng(25)
+    for page, top in ((16, 128), (32, 129), (64, 100), (128, 128), (192, 150)):
+        kv = [int(x) for x in rng.integers(0, top + 1, 30)] + [top]
+        check_attention(tpc, rng, 16, [1] * 31, kv, page)
+        check_attention(tpc, rng, 5, [0, 9, 3], [4, top, 17], page)
+        check_attention(tpc, rng, 40, [1], [top], page)
+
+
 @pytest.mark.parametrize("s", [0.01, 8.0, 60.0])
 def test_attention_score_ranges(tpc, s):
     """Nearly uniform and nearly one-hot softmaxes (scores of hundreds), whose maximum moves along the row."""

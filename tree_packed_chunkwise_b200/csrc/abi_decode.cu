@@ -180,6 +180,8 @@ int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t
     constexpr size_t smem = tpc::LatSmem<N>::total;
     TPC_CUDA(set_smem(tpc::latent_attn_tc<N>, smem));
     TPC_LAUNCH("latent_attn_tc", st, (tpc::latent_attn_tc<N><<<grid, tpc::kLatAttnThreads, smem, st>>>(tkv, tq, a)));
+    // contexts of one tile are never cut into pieces
+    if ((int64_t)lc.max_pages * lc.page_size <= tpc::kLatKT) return TPC_OK;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
