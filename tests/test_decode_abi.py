@@ -69,6 +69,7 @@ def test_append_refusals(tpc):
         assert call(c=cache(tpc, page=page)) == UNSUP, page
     assert call(c=cache(tpc, n_pages=0)) == SHAPE and call(c=cache(tpc, max_pages=0)) == SHAPE
     assert call(c=cache(tpc, n_pages=2**26)) == SHAPE and call(c=cache(tpc, max_pages=2**26)) == SHAPE
+    assert call(c=cache(tpc, page=2**31 - 64, n_pages=1, max_pages=1)) == SHAPE  # a tile past the end must not wrap
     assert call(dt=2) == UNSUP and call(r=rows(tpc, n=3)) == SHAPE
     assert call(r=rows(tpc, 0, 0, kv=None), x=None, kr=None) == 0
 

@@ -42,8 +42,9 @@ int cache_check(const char* call, const tpc_latent_cache* c, tpc::LatentCache* o
   if (c->n_pages < 1 || c->max_pages < 1) return fail(TPC_ERR_BAD_SHAPE, std::string(call) + ": n_pages and max_pages must be >= 1");
   if (!(c->page_size == 16 || c->page_size == 32 || (c->page_size >= 64 && c->page_size % 64 == 0)))
     return fail(TPC_ERR_UNSUPPORTED, std::string(call) + ": page_size must be 16, 32 or a multiple of 64");
-  if ((int64_t)c->n_pages * c->page_size > INT32_MAX || (int64_t)c->max_pages * c->page_size > INT32_MAX)
-    return fail(TPC_ERR_BAD_SHAPE, std::string(call) + ": more than 2^31 - 1 cached tokens");
+  // (room for a tile past the end)
+  if (std::max(c->n_pages, c->max_pages) > (INT32_MAX - 256) / c->page_size)
+    return fail(TPC_ERR_BAD_SHAPE, std::string(call) + ": more than 2^31 - 257 cached tokens");
   if (misaligned(c->data)) return fail(TPC_ERR_BAD_SHAPE, std::string(call) + ": the cache must be 16-byte aligned");
   *out = {(bf*)c->data, c->n_pages, c->page_size, c->block_table, c->max_pages};
   return TPC_OK;

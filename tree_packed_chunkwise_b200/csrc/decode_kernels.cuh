@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendArg
   } else {
     for (int s = r.seq + lane; s < a.rows.n_seqs; s += 32) {
       const int64_t m = (int64_t)a.rows.row_start[s + 1] - a.rows.row_start[s];
-      const int kv = min(max(a.rows.kv_len[s], 0), a.cache.max_pages * ps), p1 = (kv + ps - 1) / ps;
+      const int kv = min(max(a.rows.kv_len[s], 0), a.cache.max_pages * ps), p1 = kv > 0 ? (kv - 1) / ps + 1 : 0;
       if (m <= 0) continue;
       for (int p = s == r.seq ? pg + 1 : (int)(max((int64_t)0, kv - m) / ps); p < p1; ++p)
         clash |= a.cache.table[(size_t)s * a.cache.max_pages + p] == page;

@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     }
     for (uint64_t* b : {q_full, q_empty, done}) mbar_init(b, 1);
     *abort_flag = 0;
+    where->b = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   fence_before_sync();
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // latent_combine_kernel waits for this grid's end itself
   const uint32_t tb = *tslot;
-  LatWalk<NT> walk(a, *where, share);
+  LatWalk<NT> walk(a, *where, where->b < 0 ? 0 : share);  // (< 0: the lengths changed under the call)
   auto aborted = [&] { return *((volatile int*)abort_flag) != 0; };
   // Every wait is bounded.  After the first that runs out no role waits, copies or multiplies any
   // more, but all walk on to the end of their loops, so the barriers between the softmax warps match.
