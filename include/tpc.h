@@ -621,8 +621,8 @@ int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld
  *   lse[t][h] = log sum_j exp(scale qa[t][h] . cache_j)        (fp32 [n_rows][H], natural log).
  * A row without a token gets o = 0 and lse = -infinity.  Tokens past kv_len are never used,
  * whatever the page holds there; a latent that is not finite among the kv_len tokens can make any row
- * of its sequence NaN, rows before it included.  Scores, softmax statistics and sums in fp32; the
- * weights enter their product as bf16 and are normalised as such.  qa: [n_rows][H][576] bf16,
+ * of its sequence NaN, rows before it included.  Scores, softmax statistics and sums in fp32; a
+ * weight enters its product as two bf16 values, off by less than 2^-16 of itself.  qa: [n_rows][H][576] bf16,
  * 16-byte aligned, 1 <= H <= 128.
  *   scratch: tpc_latent_attn_scratch_bytes(H) bytes, 256-byte aligned, used by one call at a time.
  * Deterministic: the same call gives the same bits (the pieces that a long context is summed in depend

@@ -173,7 +173,7 @@ int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t
       !tensor_map(&tq, qa, tpc::kLatWidth, (uint64_t)r.n_rows * H, tpc::kLatWidth, NT))
     return fail(TPC_ERR_CUDA, "latent attention: cuTensorMapEncodeTiled failed");
   char* sc = static_cast<char*>(scratch);
-  const tpc::LatAttnArgs a{lc, r, H, scale * 1.4426950408889634f, (bf*)o, lse, (float*)sc, (float4*)(sc + tpc::kLatPartBytes),
+  const tpc::LatAttnArgs a{lc, r, H, scale * 1.4426950408889634f, (bf*)o, lse, (float*)sc, (float2*)(sc + tpc::kLatPartBytes),
                            (tpc::LatPiece*)(sc + tpc::kLatPartBytes + tpc::kLatMlBytes), status};
   const int grid = std::min(tpc_abi::sm_count(), tpc::kLatMaxCtas);
   auto go = [&](auto nt) -> int {
@@ -182,7 +182,7 @@ int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t
     TPC_CUDA(set_smem(tpc::latent_attn_tc<N>, smem));
     TPC_LAUNCH("latent_attn_tc", st, (tpc::latent_attn_tc<N><<<grid, tpc::kLatAttnThreads, smem, st>>>(tkv, tq, a)));
     // contexts of one tile are never cut into pieces
-    if ((int64_t)lc.max_pages * lc.page_size <= tpc::kLatKT) return TPC_OK;
+    if ((int64_t)lc.max_pages * lc.page_size <= tpc::LatSmem<N>::KT) return TPC_OK;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;

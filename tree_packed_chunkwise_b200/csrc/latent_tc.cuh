@@ -2,13 +2,19 @@
 //
 // Every head of every new row of a sequence reads the same cached rows [c | kr], so the (row, head)
 // pairs of a sequence are the columns of one product with the cache as its tall operand:
-//   S^T [128 tokens x NT columns] = K [128 x 576] Qa^T,   O^T [512 x NT] += C^T [512 x 128] P^T [128 x NT].
+//   S^T [KT tokens x NT columns] = K [KT x 576] Qa^T,   O^T [512 x NT] += C^T [512 x KT] P^T [KT x NT].
 // The cached tile is the MMA's A operand both times, once K-major and once (its latent part, the same
 // shared memory) MN-major, and is fetched once; the few columns are N, which the tensor core takes
 // in steps of 16 (rows as M would fill 16 of 128 lanes).  An MMA with few columns takes the time of reading
 // its A operand from shared memory, 4 KB at 128 bytes a cycle for M = 128 (measured: 36 to 58 cycles; 64 to
 // 90 when one lane of a diverged warp issues), so a tile of 128 tokens, 36 + 32 MMAs, needs 3,300 cycles of
 // the tensor core against 6,200 that its 147 KB take from HBM.
+//
+// A weight enters its product as two bf16 values, its rounding and the rounding of what that leaves (as in
+// the tree attention): one alone is off by 2^-8 at worst, more than the outputs' own rounding where tokens
+// cancel.  Up to 32 columns the two parts stand side by side as 2 NT columns of one MMA, whose time is
+// still that of its A operand; at 64 columns, where tensor memory has no room for that, they are two products
+// one after the other, and a tile is 64 tokens (KT; otherwise 128), whose parts fit beside the cached tiles.
 #pragma once
 #include <cuda.h>
 
@@ -41,6 +47,18 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint64_t* bar) {
       : "memory");
 }
 
+// as mbar_try_wait, which may suspend the thread for a while, but returns at once
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // fetches a tensor map (a __grid_constant__ parameter) ahead of its first use
 __device__ __forceinline__ void prefetch_tensor_map(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
@@ -48,37 +66,48 @@ __device__ __forceinline__ void prefetch_tensor_map(const void* tmap) {
 
 }  // namespace tc
 
-constexpr int kLatKT = 128;                         // tokens per tile
 constexpr int kLatBox = 64;                         // most rows of one TMA box
 constexpr int kLatChunks = kLatWidth / 64;          // 64-column chunks of a cached row (the last one rotary)
 constexpr int kLatItems = 1 + kLatDim / 128;        // slots of a tile: the rotary chunk, then pairs of latent chunks
 constexpr int kLatAttnThreads = 192;                // producer warp, MMA warp, four softmax warps
 constexpr int kLatMaxCtas = 148;
 constexpr int kLatMaxNT = 64;
-constexpr uint32_t kLatChunk = kLatKT * 128, kLatSlot = 2 * kLatChunk;
 
-// A tile goes through a ring of 32 KB slots, so that its slots are refilled one by one: the rotary chunk
-// once the scores have read it, each latent pair once its 128 dimensions are summed.  With four slots
-// (NT = 64) the last pair takes the rotary chunk's place.
+// A tile goes through a ring of slots of two chunks, so that its slots are refilled one by one: the rotary
+// chunk once the scores have read it, each latent pair once its 128 dimensions are summed.  At NT = 64 the
+// rotary chunk has a slot of its own and the ring holds two tiles' pairs: the next tile's scores are complete
+// before the weights of this one are there.
+// The weights P^T stand in shared memory as two bf16 operands, high parts and what they leave (low parts):
+// 64 tokens by 2 NT rows at a time, high before low.
 template <int NT>
 struct LatSmem {
-  static constexpr uint32_t slots = NT == 16 ? 6 : NT == 32 ? 5 : 4;
-  static constexpr uint32_t q = 0, ring = q + kLatChunks * NT * 128, p = ring + slots * kLatSlot, end = p + 2 * NT * 128;
+  static constexpr int KT = NT == 64 ? 64 : 128;  // tokens per tile
+  static constexpr uint32_t chunk = KT * 128, slot = 2 * chunk, slots = NT == 16 ? 6 : NT == 32 ? 5 : 8;
+  static constexpr bool own_rope = NT == 64;         // slot number `slots`
+  static constexpr int ring_items = kLatItems - own_rope;  // of a tile
+  static constexpr uint32_t q = 0, ring = q + kLatChunks * NT * 128, p = ring + slots * slot + own_rope * chunk,
+                            end = p + KT / 64 * 2 * NT * 128;
+  // item e of the CTA's tile `it`: its slot, and how many items the slot held before
+  static __device__ __forceinline__ uint32_t slot_of(int it, int e) {
+    return own_rope && e == 0 ? slots : (uint32_t)(it * ring_items + e - own_rope) % slots;
+  }
+  static __device__ __forceinline__ uint32_t uses_of(int it, int e) {
+    return own_rope && e == 0 ? it : (uint32_t)(it * ring_items + e - own_rope) / slots;
+  }
   static constexpr uint32_t red = end, fac = red + 2 * 4 * NT * 4, lim = fac + NT * 4, bars = lim + NT * 4;
-  static constexpr uint32_t total = bars + 384 + 1024;  // + slack to align the tiles to 1024 bytes
+  static constexpr uint32_t total = bars + 320;
 };
 static_assert(LatSmem<64>::total <= 232448 && LatSmem<32>::total <= 232448 && LatSmem<16>::total <= 232448,
               "shared memory of one CTA");
 
-// scratch: partial sums of the pieces (two per CTA), their (maximum, sum of the weights, sum of the rounded
-// weights), and one record per CTA
+// scratch: partial sums of the pieces (two per CTA), their (maximum, sum of the weights), and one record per CTA
 struct LatPiece {
   int col0;  // first (row, head) pair of the split unit that starts in this CTA
   int ncols;
   int n;     // its pieces: this CTA's last one, then the first ones of the next n - 1 CTAs
 };
 constexpr size_t kLatPartBytes = (size_t)kLatMaxCtas * 2 * kLatMaxNT * kLatDim * 4;
-constexpr size_t kLatMlBytes = (size_t)kLatMaxCtas * 2 * kLatMaxNT * 16;
+constexpr size_t kLatMlBytes = (size_t)kLatMaxCtas * 2 * kLatMaxNT * 8;
 constexpr size_t kLatScratch = kLatPartBytes + kLatMlBytes + ((kLatMaxCtas * sizeof(LatPiece) + 255) / 256) * 256;
 
 struct LatAttnArgs {
@@ -89,7 +118,7 @@ struct LatAttnArgs {
   __nv_bfloat16* o;
   float* lse;
   float* part;
-  float4* ml;
+  float2* ml;
   LatPiece* meta;
   int* status;
 };
@@ -126,8 +155,9 @@ __device__ __forceinline__ int lat_cts(const LatAttnArgs& a, const LatSeq& s) {
 // token tiles that the columns of column tile ct can see (at least one: the rows are written either way)
 template <int NT>
 __device__ __forceinline__ int lat_tiles(const LatAttnArgs& a, const LatSeq& s, int ct) {
+  constexpr int KT = LatSmem<NT>::KT;
   const int last = s.m == 1 ? 0 : min(((ct + 1) * NT - 1) / a.H, s.m - 1);
-  return max(1, (s.kv - s.m + last + kLatKT) / kLatKT);
+  return max(1, (s.kv - s.m + last + KT) / KT);
 }
 
 // Walks a CTA's share of the work: pieces (column tile of a sequence, range of token tiles)
@@ -237,31 +267,38 @@ __device__ __forceinline__ void round_to_smem(const uint32_t (&r)[32], uint8_t* 
 // raised when it grew by more than 8 (base 2): until then the weights are at most 2^8 and the sums of
 // the old maximum stay valid, which saves the pass over O^T.
 //
-// 64 contexts of 16,384 tokens, 16 heads: 211 us (5.72 TB/s of cache, 87 % of the copy rate; copies alone
-// 186 us), 32 heads (NT = 32, half the tokens) 128 us.  Runs of 300 rows over 4,096 tokens (NT = 64): 430
-// TFLOP/s.  A column tile of 16 where 64 fit costs 1.5 to 2.4 times (64 contexts of 4,000 tokens, 2 rows of
-// 16 heads: 78 us with 32 columns, 107 with 16; 4 rows: 104 with 64, 216 with 16), one of 64 where 16 are
-// used 1.4 times.
+// 64 contexts of 16,384 tokens, 16 heads: 213 us (5.67 TB/s of cache, 86 % of the copy rate; copies alone
+// 186 us), 32 heads (NT = 32, half the tokens) 130 us.  Runs of 300 rows over 4,096 tokens (NT = 64): 450
+// TFLOP/s (without the low parts 490, the rows' bound being the chain of scores, softmax and weighted sum).
+// Kernel times of 64 contexts of 4,000 tokens with 16, 32 and 64 columns a tile: one row of 16 heads (16
+// columns used) 65, 73 and 92 us; 2 rows 105, 75 and 92; 4 rows 214, 126 and 94.
 template <int NT>
 __global__ void __launch_bounds__(kLatAttnThreads, 1)
     latent_attn_tc(const __grid_constant__ CUtensorMap tma_kv, const __grid_constant__ CUtensorMap tma_q, LatAttnArgs a) {
   using namespace tc;
   using L = LatSmem<NT>;
-  constexpr int R = NT / 8, U = L::slots;
-  constexpr uint32_t kTmem = NT == 16 ? 128 : NT == 32 ? 256 : 512;
+  constexpr int R = NT / 8, U = L::slots, KT = L::KT, G = KT / 64;  // G: 16-token groups of a softmax warp
+  // columns of an accumulator of O^T: products with the high and the low parts side by side where they fit
+  constexpr int W = NT == 64 ? NT : 2 * NT;
+  constexpr uint32_t kTmem = NT == 16 ? 256 : 512, kScores = 4 * W;
   extern __shared__ __align__(1024) uint8_t lsm_raw[];
-  uint8_t* sm = lsm_raw + ((1024u - (smem_u32(lsm_raw) & 1023u)) & 1023u);
+  uint8_t* sm = lsm_raw;
   const uint32_t sb = smem_u32(sm);
+  if (sb & 1023u) {  // the tiles need the alignment that the array asks for (there is no room to correct it)
+    set_status(a.status, kStatusCheck);
+    if (threadIdx.x == 0) a.meta[blockIdx.x].n = 0;
+    return;
+  }
   float* red = reinterpret_cast<float*>(sm + L::red);
   float* fac = reinterpret_cast<float*>(sm + L::fac);
   int* lim = reinterpret_cast<int*>(sm + L::lim);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
-  uint64_t *full = bars, *empty = bars + 6, *s_full = bars + 12, *p_full = bars + 14, *o_done = bars + 16,
-           *q_full = bars + 18, *q_empty = bars + 19, *done = bars + 20;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 21);
-  int* abort_flag = reinterpret_cast<int*>(bars + 21) + 1;
-  LatStart* where = reinterpret_cast<LatStart*>(bars + 22);
-  long long* sums = reinterpret_cast<long long*>(bars + 25);  // per warp
+  uint64_t *full = bars, *empty = bars + 9, *s_full = bars + 18, *p_full = bars + 20, *o_done = bars + 22,
+           *q_full = bars + 24, *q_empty = bars + 25, *done = bars + 26;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 27);
+  int* abort_flag = reinterpret_cast<int*>(bars + 27) + 1;
+  LatStart* where = reinterpret_cast<LatStart*>(bars + 28);
+  long long* sums = reinterpret_cast<long long*>(bars + 31);  // per warp
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     prefetch_tensor_map(&tma_kv);
@@ -288,7 +325,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
   if (lane == 31) sums[w] = incl;
   if (w == 1) tmem_alloc(tslot, kTmem);
   if (tid == 0) {
-    for (int i = 0; i < U; ++i) {
+    for (int i = 0; i < U + L::own_rope; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -354,8 +391,8 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     auto fetch = [&]() -> Tile {   // only loads the page number: it is looked at a tile later
       Tile t{walk.left > 0, ahead == 0, 0, 0, 0, 0};
       if (!t.valid) return t;
-      const int t0 = (walk.t0 + ahead) * kLatKT;
-      t.segs = (min(max(walk.s.kv - t0, 0), kLatKT) + box - 1) / box;
+      const int t0 = (walk.t0 + ahead) * KT;
+      t.segs = (min(max(walk.s.kv - t0, 0), KT) + box - 1) / box;
       t.q_row = walk.s.row0 * a.H + walk.ct * NT;
       if (lane < t.segs) {
         const int tok = t0 + lane * box;
@@ -368,7 +405,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       }
       return t;
     };
-    int item = 0, piece = -1;
+    int it = 0, piece = -1;
     Tile cur = fetch(), nxt = cur;
     while (cur.valid) {
       if (cur.page < 0 || cur.page >= a.cache.n_pages) {
@@ -384,10 +421,11 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
           if (lane < kLatChunks) tma_load_2d(sm + L::q + lane * NT * 128, &tma_q, 64 * lane, cur.q_row, q_full);
         }
       }
-      for (int e = 0; e < kLatItems; ++e, ++item) {
-        const int st = item % U, nc = e == 0 ? 1 : 2;  // chunks of the item: 8, then 0 1, 2 3, 4 5, 6 7
+      for (int e = 0; e < kLatItems; ++e) {
+        const uint32_t st = L::slot_of(it, e), uses = L::uses_of(it, e);
+        const int nc = e == 0 ? 1 : 2;  // chunks of the item: 8, then 0 1, 2 3, 4 5, 6 7
         if (e == 1) nxt = fetch();
-        const bool ok = item < U || wait(&empty[st], (item / U - 1) & 1);
+        const bool ok = uses == 0 || wait(&empty[st], (uses - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) continue;
         if (lane == 0) {
           if (cur.segs)
@@ -399,25 +437,27 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
         const int seg = lane / nc, c = lane % nc;
         const int row = __shfl_sync(0xffffffffu, my_row, seg);
         if (seg < cur.segs)
-          tma_load_2d(sm + L::ring + st * kLatSlot + c * kLatChunk + seg * box * 128, &tma_kv,
+          tma_load_2d(sm + L::ring + st * L::slot + c * L::chunk + seg * box * 128, &tma_kv,
                       64 * (e == 0 ? kLatChunks - 1 : 2 * (e - 1) + c), row, &full[st]);
       }
       cur = nxt;
+      ++it;
     }
     if (aborted() && lane == 0) {  // copies in flight land before the CTA ends
-      for (int i = max(0, item - U); i < item; ++i) mbar_wait(&full[i % U], (i / U) & 1, 100000000ull);
+      for (int i = max(0, it * L::ring_items - U); i < it * L::ring_items; ++i) mbar_wait(&full[i % U], (i / U) & 1, 100000000ull);
+      if (L::own_rope && it > 0) mbar_wait(&full[U], (it - 1) & 1, 100000000ull);
       if (piece >= 0) mbar_wait(q_full, piece & 1, 100000000ull);
     }
   } else if (w == 1) {  // ---- MMA
     // The whole warp walks the loops and one elected lane issues, so that descriptors stay in uniform
     // registers.
     const uint32_t lead = elect_one();
-    constexpr uint32_t id_s = idesc_bf16(128, NT, false, false), id_o = idesc_bf16(128, NT, true, false);
+    constexpr uint32_t id_s = idesc_bf16(KT, NT, false, false), id_o = idesc_bf16(128, W, true, false);
     // descriptors of slot 0 and of step 0; the low word holds address / 16
-    const uint64_t d_kv_k = sw_desc_k(sb + L::ring, kLatKT, 0), d_kv_mn = sw_desc_mn(sb + L::ring, kLatKT, 0);
-    const uint64_t d_q = sw_desc_k(sb + L::q, NT, 0), d_p = sw_desc_k(sb + L::p, NT, 0);
+    const uint64_t d_kv_k = sw_desc_k(sb + L::ring, KT, 0), d_kv_mn = sw_desc_mn(sb + L::ring, KT, 0);
+    const uint64_t d_q = sw_desc_k(sb + L::q, NT, 0), d_p = sw_desc_k(sb + L::p, 2 * NT, 0);
     auto k_step = [](int rows, int ks) { return (uint64_t)(((ks >> 2) * rows * 128 + (ks & 3) * 32) >> 4); };
-    int it = 0, piece = 0, slot = 0, pend = -1;  // slot: of the next item; pend: tile whose weighted sum is not issued yet
+    int it = 0, piece = 0, slot = 0, pend = -1;  // slot: of the next item in the ring; pend: tile whose weighted sum is not issued yet
     int pend_slot = 0;                           // slot of its first latent pair
     uint32_t pend_acc = 0;
     auto weighted_sum = [&] {  // O^T (+)= C^T P^T of the pending tile
@@ -425,53 +465,79 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       int st = pend_slot;
 #pragma unroll
       for (int mb = 0; mb < 4; ++mb) {
-        const uint64_t d = d_kv_mn + (uint64_t)(st * (kLatSlot >> 4));
+        const uint64_t d = d_kv_mn + (uint64_t)(st * (L::slot >> 4));
 #pragma unroll
-        for (int ks = 0; ks < kLatKT / 16; ++ks)
-          mma_bf16_if(lead, tb + mb * NT, d + (uint64_t)(ks * (2048 >> 4)), d_p + k_step(NT, ks), id_o, ks ? 1u : pend_acc);
+        for (int part = 0; part < 2 * NT / W; ++part)
+#pragma unroll
+          for (int ks = 0; ks < KT / 16; ++ks)
+            mma_bf16_if(lead, tb + mb * W, d + (uint64_t)(ks * (2048 >> 4)), d_p + (uint64_t)(part * (W * 128 >> 4)) + k_step(2 * NT, ks),
+                        id_o, part || ks ? 1u : pend_acc);
         if (mb == 3) commit_if(lead, &o_done[pend & 1]);
         commit_if(lead, &empty[st]);
         st = st + 1 == U ? 0 : st + 1;
       }
       pend = -1;
     };
-    // waits for the barrier and issues the pending sum meanwhile, on which the barrier may depend
-    auto wait_or_sum = [&](uint64_t* bar, uint32_t parity) -> bool {
+    // Waits for item e of tile `it` (ready: bits of items known to be there) and, with it, for the piece's
+    // queries, and issues the pending sum meanwhile, on which they may depend.
+    uint32_t ready = 0;
+    auto wait_item = [&](int e) -> bool {
+      const uint32_t queries = 1u << (kLatItems + 1), need = 1u << e | queries;
       uint64_t t0 = 0;
-      while (!__any_sync(0xffffffffu, aborted())) {
-        if (pend >= 0 && __all_sync(0xffffffffu, mbar_try_wait(&p_full[pend & 1], (pend >> 1) & 1))) weighted_sum();
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+      while ((ready & need) != need) {
+        if constexpr (NT == 64) {
+          // One look at a barrier takes 200 to 400 cycles of the warp that also issues the MMAs, so every lane
+          // looks at another one: the items of the tile (their slots' earlier copies have been waited for), the
+          // pending weights, the queries.  Runs of 300 rows over 4,096 tokens 361 us, one look after the other 414.
+          bool up = false;
+          if (lane < kLatItems)
+            up = mbar_test_wait(&full[L::slot_of(it, lane)], L::uses_of(it, lane) & 1);
+          else if (lane == kLatItems)
+            up = pend >= 0 && mbar_test_wait(&p_full[pend & 1], (pend >> 1) & 1);
+          else if (lane == kLatItems + 1)
+            up = mbar_test_wait(q_full, piece & 1);
+          ready = __ballot_sync(0xffffffffu, up);
+          __syncwarp();
+          if (ready >> kLatItems & 1) weighted_sum();
+        } else {
+          // (bound by the copies: looks that suspend the warp, 64 x 16,384 tokens 210 us, otherwise 219)
+          if (pend >= 0 && __all_sync(0xffffffffu, mbar_try_wait(&p_full[pend & 1], (pend >> 1) & 1))) weighted_sum();
+          if (!(ready & queries) && __all_sync(0xffffffffu, mbar_try_wait(q_full, piece & 1))) ready |= queries;
+          if (__all_sync(0xffffffffu, mbar_try_wait(&full[L::slot_of(it, e)], L::uses_of(it, e) & 1))) ready |= 1u << e;
+        }
+        if ((ready & need) == need) break;
+        if (__any_sync(0xffffffffu, aborted())) return false;
         const uint64_t t = globaltimer();
         if (t0 == 0) t0 = t;
         if (t - t0 > 2000000000ull) give_up();
       }
-      return false;
+      return true;
     };
     auto sum_now = [&] {
       if (pend >= 0 && __all_sync(0xffffffffu, wait(&p_full[pend & 1], (pend >> 1) & 1))) weighted_sum();
     };
     // (loop bounds read from one lane: the compiler then knows that the warp agrees on them)
     for (; __shfl_sync(0xffffffffu, walk.left > 0, 0); walk.next(), ++piece) {
-      wait_or_sum(q_full, piece & 1);
       const int n = __shfl_sync(0xffffffffu, walk.n, 0);
       for (int i = 0; i < n; ++i, ++it) {
-        const uint32_t acc = tb + 4 * NT + (it & 1) * NT;
+        const uint32_t acc = tb + kScores + (it & 1) * NT;
 #pragma unroll
         for (int e = 0; e < kLatItems; ++e) {
-          const int st = slot;
-          slot = slot + 1 == U ? 0 : slot + 1;
-          if (!wait_or_sum(&full[st], ((it * kLatItems + e) / U) & 1)) continue;
+          const int st = L::own_rope && e == 0 ? U : slot;
+          if (st == slot) slot = slot + 1 == U ? 0 : slot + 1;
+          if (e == 0) ready = NT == 64 || i == 0 ? 0u : 1u << (kLatItems + 1);
+          if (!wait_item(e)) continue;
           fence_after_sync();
-          const uint64_t d = d_kv_k + (uint64_t)(st * (kLatSlot >> 4));
+          const uint64_t d = d_kv_k + (uint64_t)(st * (L::slot >> 4));
           if (e == 0) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_if(lead, acc, d + k_step(kLatKT, ks), d_q + k_step(NT, 4 * (kLatChunks - 1) + ks), id_s, ks ? 1u : 0u);
+              mma_bf16_if(lead, acc, d + k_step(KT, ks), d_q + k_step(NT, 4 * (kLatChunks - 1) + ks), id_s, ks ? 1u : 0u);
             commit_if(lead, &empty[st]);
           } else {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              mma_bf16_if(lead, acc, d + k_step(kLatKT, ks), d_q + k_step(NT, 8 * (e - 1) + ks), id_s, 1u);
+              mma_bf16_if(lead, acc, d + k_step(KT, ks), d_q + k_step(NT, 8 * (e - 1) + ks), id_s, 1u);
           }
         }
         if (!__any_sync(0xffffffffu, aborted())) {
@@ -488,9 +554,9 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     commit_if(lead, done);
     if (!mbar_wait(done, 0, 2000000000ull)) set_status(a.status, 8);
     __syncwarp();
-  } else {  // ---- softmax warps: sub-partition sp holds tokens 32 sp .. 32 sp + 31 of a tile, and
+  } else {  // ---- softmax warps: sub-partition sp holds tokens 16 G sp .. 16 G sp + 16 G - 1 of a tile, and
             //      latent dimensions 32 sp .. 32 sp + 31 of each 128-row block of O^T
-    const int sp = w & 3, k0 = 32 * sp + (lane >> 2), st = tid - 64;
+    const int sp = w & 3, k0 = 16 * G * sp + (lane >> 2), st = tid - 64;
     const uint32_t la = tb + ((uint32_t)(32 * sp) << 16);
     auto meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
     int it = 0;
@@ -501,29 +567,29 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       // last visible position of every column (columns past the run's end take its last row's)
       if (st < NT) lim[st] = s.kv - s.m + min((walk.ct * NT + st) / a.H, s.m - 1);
       const int lim0 = s.kv - s.m + walk.ct * NT / a.H;
-      float mx[2 * R], sum[2 * R], sumr[2 * R];
+      float mx[2 * R], sum[2 * R];
 #pragma unroll
       for (int c = 0; c < 2 * R; ++c) {
         mx[c] = -INFINITY;
-        sum[c] = sumr[c] = 0.f;
+        sum[c] = 0.f;
       }
       meet();  // lim is set; the last piece's reads of red and fac are over
       for (int i = 0; i < walk.n; ++i, ++it) {
-        const int t0 = (walk.t0 + i) * kLatKT;
+        const int t0 = (walk.t0 + i) * KT;
         wait(&s_full[it & 1], (it >> 1) & 1);
         __syncwarp();
         fence_after_sync();
-        float x[2][4 * R];  // [16-token half][...]
-        tmem_ld_16x256<R>(la + 4 * NT + (it & 1) * NT, x[0]);
-        tmem_ld_16x256<R>(la + (16u << 16) + 4 * NT + (it & 1) * NT, x[1]);
-        const bool mask = t0 + kLatKT - 1 > lim0;
+        float x[G][4 * R];  // [16-token group][...]; the rows of an M = 64 accumulator are lanes 0 .. 15 of a sub-partition
+#pragma unroll
+        for (int g = 0; g < G; ++g) tmem_ld_16x256<R>(la + ((uint32_t)(16 * g) << 16) + kScores + (it & 1) * NT, x[g]);
+        const bool mask = t0 + KT - 1 > lim0;
         float tm[2 * R];
 #pragma unroll
         for (int c = 0; c < 2 * R; ++c) {  // maximum of each column over the tile
           float v = -INFINITY;
           const int last = mask ? lim[8 * (c >> 1) + 2 * (lane & 3) + (c & 1)] : 0;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          for (int g = 0; g < 2 * G; ++g) {
             float& y = x[g >> 1][4 * (c >> 1) + 2 * (g & 1) + (c & 1)];
             y = mask && t0 + k0 + 8 * g > last ? -INFINITY : y * a.scale_log2;
             v = fmaxf(v, y);
@@ -562,7 +628,6 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
             const float f = m2 == -INFINITY ? 1.f : ex2(mx[c] - m2);
             mx[c] = m2;
             sum[c] *= f;
-            sumr[c] *= f;
             tm[c] = f;
           }
         }
@@ -578,7 +643,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
             }
             meet();
 #pragma unroll 1
-            for (int c0 = 0; c0 < 4 * NT; c0 += 16) {
+            for (int c0 = 0; c0 < 4 * W; c0 += 16) {
               float v[16];
               tmem_ld16(la + c0, v);
 #pragma unroll
@@ -587,41 +652,42 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
             }
           }
         }
-        // weights: fp32 into the sum of the log-sum-exp, bf16 into the product (the tensor core's operand
-        // type).  The product is divided by the sum of the rounded weights, so that what is summed has weights
-        // of sum 1: a row that one token dominates is as exact as that token.
+        // weights: fp32 into their sum; into the product as two bf16 values (the tensor core's operand type),
+        // the second holding what the first leaves, so that a weight is off by less than 2^-16 of itself
 #pragma unroll
         for (int c = 0; c < 2 * R; ++c) {
           const float m = mx[c] == -INFINITY ? 0.f : mx[c];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          for (int g = 0; g < 2 * G; ++g) {
             float& y = x[g >> 1][4 * (c >> 1) + 2 * (g & 1) + (c & 1)];
             y = ex2(y - m);
             sum[c] += y;
           }
         }
-        const uint32_t ph = sb + L::p + (sp >> 1) * NT * 128;
+        const uint32_t ph = sb + L::p + (16 * G * sp / 64) * 2 * NT * 128;
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < G; ++g)
 #pragma unroll
           for (int j = 0; j < R; j += 2) {
-            const int n = 8 * (j + (lane >> 4)) + (lane & 7), unit = 4 * (sp & 1) + 2 * g + ((lane >> 3) & 1);
-            uint32_t p[4];
+            const int n = 8 * (j + (lane >> 4)) + (lane & 7), unit = 2 * ((G * sp + g) & 3) + ((lane >> 3) & 1);
+            const uint32_t at = ph + n * 128 + ((unit ^ (lane & 7)) << 4);
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              p[e] = pack_bf16(x[g][4 * j + 2 * e], x[g][4 * j + 2 * e + 1]);
-              sumr[2 * j + (e & 2)] += __uint_as_float(p[e] << 16);
-              sumr[2 * j + (e & 2) + 1] += __uint_as_float(p[e] & 0xffff0000u);
+              const float y0 = x[g][4 * j + 2 * e], y1 = x[g][4 * j + 2 * e + 1];
+              hi[e] = pack_bf16(y0, y1);
+              lo[e] = pack_bf16(y0 - __uint_as_float(hi[e] << 16), y1 - __uint_as_float(hi[e] & 0xffff0000u));
             }
-            stmatrix4_trans(ph + n * 128 + ((unit ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+            stmatrix4_trans(at, hi[0], hi[1], hi[2], hi[3]);
+            stmatrix4_trans(at + NT * 128, lo[0], lo[1], lo[2], lo[3]);
           }
         // rows of the tile that hold no token of the sequence: their weights are 0, but whatever the
         // page holds there (NaN among it) must not meet them
         const int have = max(s.kv - t0, 0);
-        if (have < kLatKT) {
-          const int per_chunk = (kLatKT - have) * 8;
+        if (have < KT) {
+          const int per_chunk = (KT - have) * 8;
           for (int c = 0; c < kLatDim / 64; ++c) {
-            uint8_t* row = sm + L::ring + ((it * kLatItems + 1 + (c >> 1)) % U) * kLatSlot + (c & 1) * kLatChunk + have * 128;
+            uint8_t* row = sm + L::ring + L::slot_of(it, 1 + (c >> 1)) * L::slot + (c & 1) * L::chunk + have * 128;
             for (int u = st; u < per_chunk; u += 128) *reinterpret_cast<uint4*>(row + u * 16) = make_uint4(0, 0, 0, 0);
           }
         }
@@ -634,50 +700,50 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
 #pragma unroll
       for (int c = 0; c < 2 * R; ++c) {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], d);
-          sumr[c] += __shfl_xor_sync(0xffffffffu, sumr[c], d);
-        }
+        for (int d = 4; d < 32; d <<= 1) sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], d);
       }
       meet();  // red and fac have been read
       if (lane < 4) {
 #pragma unroll
         for (int j = 0; j < R; ++j) {
           *reinterpret_cast<float2*>(red + sp * NT + 8 * j + 2 * lane) = make_float2(sum[2 * j], sum[2 * j + 1]);
-          *reinterpret_cast<float2*>(red + (4 + sp) * NT + 8 * j + 2 * lane) = make_float2(sumr[2 * j], sumr[2 * j + 1]);
           if (sp == 0) *reinterpret_cast<float2*>(fac + 8 * j + 2 * lane) = make_float2(mx[2 * j], mx[2 * j + 1]);
         }
       }
       meet();
       const bool whole = walk.t0 == 0 && walk.n == walk.tiles;
       const int slot = 2 * blockIdx.x + (walk.t0 == 0 ? 1 : 0);
-      float l = 0.f, lr = 0.f;
+      float l = 0.f;
       if (st < NT)
-        for (int i = 0; i < 4; ++i) {
-          l += red[i * NT + st];
-          lr += red[(4 + i) * NT + st];
-        }
+        for (int i = 0; i < 4; ++i) l += red[i * NT + st];
       if (st < ncols) {
         if (whole)
           a.lse[col0 + st] = l == 0.f ? -INFINITY : (fac[st] + log2f(l)) * 0.6931471805599453f;
         else
-          a.ml[slot * kLatMaxNT + st] = make_float4(fac[st], l, lr, 0.f);
+          a.ml[slot * kLatMaxNT + st] = make_float2(fac[st], l);
       }
       if (!whole && walk.t0 == 0 && st == 0) {
         const long long rest = walk.tiles - walk.n;
         a.meta[blockIdx.x] = {col0, ncols, 1 + (int)((rest + per - 1) / per)};
       }
       meet();
-      if (st < NT) fac[st] = !whole ? 1.f : lr == 0.f ? 0.f : 1.f / lr;
+      if (st < NT) fac[st] = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
       meet();
       wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
       __syncwarp();
       fence_after_sync();
 #pragma unroll 1
       for (int c0 = 0; c0 < 4 * NT; c0 += 16) {
+        const int cc = c0 % NT;
         float v[16];
-        tmem_ld16(la + c0, v);
-        const int cc = c0 % NT, dim = c0 / NT * 128 + 32 * sp + lane;
+        tmem_ld16(la + c0 / NT * W + cc, v);
+        if constexpr (W == 2 * NT) {
+          float v2[16];
+          tmem_ld16(la + c0 / NT * W + NT + cc, v2);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) v[c] += v2[c];
+        }
+        const int dim = c0 / NT * 128 + 32 * sp + lane;
         if (whole) {
 #pragma unroll
           for (int c = 0; c < 16; ++c)
@@ -697,15 +763,16 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
 }
 
 // Joins the pieces of every unit that starts in one share and ends in a later one:
-//   o = sum_i e^{m_i - m} O_i / sum_i e^{m_i - m} r_i  (r: sums of the rounded weights; lse from the others),
+//   o = sum_i e^{m_i - m} O_i / sum_i e^{m_i - m} l_i,
 // in an order that depends on the number of pieces alone.  Launched while the attention kernel still
 // runs (it waits for that grid's end).  Its time is that of a chain of loads, so a thread takes at most
 // 4 to 10 pieces, mostly loaded at once, and the CTAs share a list of work items of three kinds:
 //   up to 4 pieces (ragged batches, most units): four columns, 128 threads x 4 dimensions each;
 //   up to 32 (a few contexts): one column, a group of 128 threads for every fourth piece;
 //   more (one context over all CTAs): 128 dimensions of a column, a warp for every 16th piece.
-// Whole calls of 8 contexts of 4000 tokens with 64 columns: 25.2 us; with up to 8 pieces a thread (one CTA
-// an SM for its registers) 30.4, with the last kind for all above 8 pieces 46.  One context of 6000
+// Whole calls of 8 contexts of 4000 tokens with 64 columns, while single bf16 weights went into 128-token
+// tiles: 25.2 us; with up to 8 pieces a thread (one CTA an SM for its registers) 30.4, with the last kind
+// for all above 8 pieces 46.  One context of 6000
 // tokens: 14 us, and 34 with one CTA per column.
 constexpr int kLatCombThreads = 512, kLatCombFew = 4, kLatCombSome = 32;
 
@@ -717,8 +784,8 @@ struct LatJoin {  // running sum of pieces for 4 dimensions of a column
     o.z = fmaf(e, x.z, o.z);
     o.w = fmaf(e, x.w, o.w);
   }
-  __device__ __forceinline__ void store(const LatAttnArgs& a, size_t col, int d, float m, float l, float r) const {
-    const float inv = r == 0.f ? 0.f : 1.f / r;
+  __device__ __forceinline__ void store(const LatAttnArgs& a, size_t col, int d, float m, float l) const {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     store4(a.o + col * kLatDim + d, v);
     if (d == 0) a.lse[col] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -761,8 +828,8 @@ __global__ void __launch_bounds__(kLatCombThreads, 2) latent_combine_kernel(LatA
     if (u.n <= kLatCombFew) {
       const int c = 4 * k + (tid >> 7), d = 4 * (tid & 127);
       if (c >= u.ncols) continue;
-      float m = -INFINITY, l = 0.f, r = 0.f;
-      float4 ml[kLatCombFew];
+      float m = -INFINITY, l = 0.f;
+      float2 ml[kLatCombFew];
       float4 x[kLatCombFew];
 #pragma unroll
       for (int i = 0; i < kLatCombFew; ++i)
@@ -777,33 +844,28 @@ __global__ void __launch_bounds__(kLatCombThreads, 2) latent_combine_kernel(LatA
         if (i < u.n) {
           const float e = tc::ex2(ml[i].x - m);
           l = fmaf(e, ml[i].y, l);
-          r = fmaf(e, ml[i].z, r);
           join.add(e, x[i]);
         }
-      join.store(a, (size_t)u.col0 + c, d, m, l, r);
+      join.store(a, (size_t)u.col0 + c, d, m, l);
       continue;
     }
     // G groups of threads, group g takes pieces g, g + G, ...; d: the thread's dimensions
     const bool some = u.n <= kLatCombSome;
     const int c = some ? k : k >> 2, d = some ? 4 * (tid & 127) : 128 * (k & 3) + 4 * lane;
     const int G = some ? kLatCombThreads / 128 : kLatCombThreads / 32, g = some ? tid >> 7 : w;
-    float m = -INFINITY, l = 0.f, r = 0.f;
+    float m = -INFINITY, l = 0.f;
     for (int i = lane; i < u.n; i += 32) m = fmaxf(m, a.ml[slot(i) + c].x);
 #pragma unroll
     for (int e = 16; e; e >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
     if (m == -INFINITY) m = 0.f;
     for (int i = lane; i < u.n; i += 32) {
-      const float4 ml = a.ml[slot(i) + c];
+      const float2 ml = a.ml[slot(i) + c];
       const float e = tc::ex2(ml.x - m);
       if (w == 0) f[i] = e;
       l = fmaf(e, ml.y, l);
-      r = fmaf(e, ml.z, r);
     }
 #pragma unroll
-    for (int e = 16; e; e >>= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, e);
-      r += __shfl_xor_sync(0xffffffffu, r, e);
-    }
+    for (int e = 16; e; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
     __syncthreads();
 #pragma unroll 5
     for (int i = g; i < u.n; i += G)
@@ -814,7 +876,7 @@ __global__ void __launch_bounds__(kLatCombThreads, 2) latent_combine_kernel(LatA
       const int step = kLatCombThreads / G;
 #pragma unroll 3
       for (int i = 1; i < G; ++i) join.add(1.f, acc_s[step * i + tid]);
-      join.store(a, (size_t)u.col0 + c, d, m, l, r);
+      join.store(a, (size_t)u.col0 + c, d, m, l);
     }
     __syncthreads();  // f and acc_s are free again
   }
