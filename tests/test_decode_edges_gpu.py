@@ -56,3 +56,36 @@ def test_attention_of_cancelling_tokens(tpc, H, m, L):
     ref, lref, oa, _ = od.attention(host(qa), host(cache), table, [kv], 1.0, [0, m])
     within(host(o), ref, UBF * np.abs(ref) + (2.0 ** -14 + 2.0 ** -16 + kv * U32) * oa, "o")
     within(host(lse), lref, 2.0 ** -18 + kv * U32 + 4 * U32 * np.abs(lref), "lse")
+
+
+# ------------------------------------------------------------------------------------ rows of other sequences and of none
+@pytest.mark.parametrize("H,m", [(5, 1), (5, 3), (16, 1), (24, 1), (24, 2), (40, 1), (5, 13)])
+def test_attention_rows_that_a_unit_does_not_own(tpc, H, m):
+    """The bits of a sequence's outputs depend on its own rows alone, whatever the rows behind the last sequence
+    hold and whatever the next sequence asks.  Scores rise along the context, slowly for every second sequence and
+    by more than the running maximum's slack in every tile for the others; the shares are several tiles long."""
+    import torch
+    rng = np.random.default_rng(H + m)
+    page, kv, extra, B = 64, 700, 16, 120
+    cache, _ = rounded(rng, 11, page, 576, dtype=torch.bfloat16)
+    cache[:, :, 0] = torch.arange(11 * page, device="cuda").view(11, page).bfloat16() / 4
+    table = i32(np.broadcast_to(np.arange(11), (B, 11)))
+    mine = (torch.arange(B, device="cuda") % 2 == 0).repeat_interleave(m)
+    qa, _ = rounded(rng, B * m + extra, H, 576, dtype=torch.bfloat16, s=0.05)
+    qa[:, :, 0] = 8.0
+    qa[:B * m][mine, :, 0] = 0.02
+    status = new_status()
+    got = []
+    for fill in (None, 0.0, 300.0, float("inf"), float("-inf"), float("nan")):
+        q = qa.clone()
+        if fill is not None:
+            q[B * m:] = fill
+            q[:B * m][~mine] *= -1.0
+        o = torch.full((len(q), H, 512), -7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((len(q), H), -7.0, device="cuda")
+        tpc.tpc_latent_attn(q, cache, table, i32([kv] * B), 1.0, row_start=i32(np.arange(B + 1) * m), o=o, lse=lse, status=status)
+        assert bool((o[B * m:] == -7).all()) and bool((lse[B * m:] == -7).all())
+        got.append((o[:B * m][mine], lse[:B * m][mine]))
+    assert status.item() == 0 and bool(torch.isfinite(got[0][0].float()).all())
+    for o, lse in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])

@@ -261,10 +261,10 @@ __device__ __forceinline__ void round_to_smem(const uint32_t (&r)[32], uint8_t* 
 //
 // Warp 0 fetches tiles by TMA (64-column boxes, one per page and column chunk) into the ring (a prefetch
 // of the next tile into L2 beside it measured 2 % slower).  Warp 1 issues the MMAs: the scores of tile i + 1 as far as its slots have arrived, and the weighted sum of
-// tile i as soon as the weights are there.  Warps 2-5 run the softmax: a warp holds 32 tokens x NT
+// tile i as soon as the weights are there.  Warps 2-5 run the softmax: a warp holds KT / 4 tokens x NT
 // columns of S^T in the 16x256b register layout, maxima over tokens are 3 shuffles and one exchange
-// between the four warps.  Running sums stay per lane until the piece ends.  The maximum is only
-// raised when it grew by more than 8 (base 2): until then the weights are at most 2^8 and the sums of
+// between the four warps.  Running sums stay per lane until the piece ends.  A column's maximum is only
+// raised when it grew by more than 8 (base 2): until then its weights are at most 2^8 and the sums of
 // the old maximum stay valid, which saves the pass over O^T.
 //
 // 64 contexts of 16,384 tokens, 16 heads: 213 us (5.67 TB/s of cache, 86 % of the copy rate; copies alone
@@ -570,7 +570,9 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       float mx[2 * R], sum[2 * R];
 #pragma unroll
       for (int c = 0; c < 2 * R; ++c) {
-        mx[c] = -INFINITY;
+        // columns past the unit's own hold queries of other sequences, or of rows outside every one: with
+        // this maximum they never ask for a pass over O^T
+        mx[c] = 8 * (c >> 1) + 2 * (lane & 3) + (c & 1) < ncols ? -INFINITY : INFINITY;
         sum[c] = 0.f;
       }
       meet();  // lim is set; the last piece's reads of red and fac are over
@@ -623,10 +625,10 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
         grew = __any_sync(0xffffffffu, grew);
         if (grew) {
 #pragma unroll
-          for (int c = 0; c < 2 * R; ++c) {
-            const float m2 = fmaxf(mx[c], tm[c]);
-            const float f = m2 == -INFINITY ? 1.f : ex2(mx[c] - m2);
-            mx[c] = m2;
+          for (int c = 0; c < 2 * R; ++c) {  // (only columns that grew: a column's results depend on itself alone)
+            const bool up = tm[c] > mx[c] + 8.f;
+            const float f = up ? ex2(mx[c] - tm[c]) : 1.f;
+            if (up) mx[c] = tm[c];
             sum[c] *= f;
             tm[c] = f;
           }
