@@ -531,7 +531,8 @@ int tpc_group_status(const tpc_plan* plan, const tpc_group_shape* shape, void* w
  * 0 .. n_rows).  row_start NULL: one row each, n_rows == n_seqs.  Nothing of rows outside every
  * sequence is used, and their outputs are left as they were.  kv_len[b] counts the cached tokens of
  * sequence b, its new rows included, so new row i of m is at position kv_len[b] - m + i; a row at a
- * negative position (kv_len 0: a padding entry of the batch) has no token.  row_start, kv_len and
+ * negative position (kv_len 0: a padding entry of the batch) has no token.  A sequence whose rows are
+ * not within 0 .. n_rows, or whose row_start decreases, is skipped and recorded.  row_start, kv_len and
  * the block table are device memory, read when the kernels run, so that a captured graph can be
  * replayed with new values.
  *

@@ -89,3 +89,79 @@ def test_attention_rows_that_a_unit_does_not_own(tpc, H, m):
     assert status.item() == 0 and bool(torch.isfinite(got[0][0].float()).all())
     for o, lse in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+# ------------------------------------------------------------------------------------ malformed row tables
+@pytest.mark.parametrize("start", [[0, 1, 2, 9], [-4, 1, 2, 3], [3, 2, 1, 0], [0, 2, 1, 3], [2 ** 31 - 1, 0, 1, 3], [0, -2 ** 31 + 1, 2 ** 31 - 1, 3],
+                                   [0, 1, 3, 4], [0, 0, 7, 3]])
+def test_bad_row_starts_are_skipped_and_reported_by_every_call(tpc, start):
+    """A sequence whose rows are not within 0 .. n_rows, or decrease, has no rows: append leaves its cached tokens
+    and absorb its outputs as they were, the others are right (unless two sequences claim a row), and each call by
+    itself sets the status."""
+    import torch
+    rng = np.random.default_rng(abs(start[0]) % 97 + start[-1])
+    H, n, page, kv = 3, 3, 16, [20, 9, 31]
+    table = rng.permutation(6).reshape(3, 2).astype(np.int32)
+    good = [b for b in range(3) if 0 <= start[b] <= start[b + 1] <= n]
+    claims = [[b for b in good if start[b] <= t < start[b + 1]] for t in range(n)]
+    c, c64 = rounded(rng, n, 512, dtype=torch.bfloat16)
+    kr, k64 = rounded(rng, n, 64, dtype=torch.bfloat16)
+    cache, before = rounded(rng, 6, page, 576, dtype=torch.bfloat16)
+    status = new_status()
+    tpc.tpc_latent_append(cache, i32(table), i32(kv), c, kr, row_start=i32(start), status=status)
+    assert status.item() == 7
+    want, free = before.copy(), np.zeros((6, page), bool)
+    for b in good:
+        for i in range(start[b + 1] - start[b]):
+            p, t = kv[b] - (start[b + 1] - start[b]) + i, start[b] + i
+            at = table[b, p // page], p % page
+            if claims[t] == [b]:
+                want[at] = np.concatenate([c64[t], od.rotate(k64[t], p)])
+            else:
+                free[at] = True
+    x = host(cache)
+    assert np.array_equal(x[..., :512][~free], want[..., :512][~free])
+    tol = UBF * np.abs(want[..., 512:]) + 2.0 ** -19 * np.abs(k64).max()
+    within(x[..., 512:][~free], want[..., 512:][~free], tol[~free], "rotary key")
+
+    q, q64 = rounded(rng, n, H, 192, dtype=torch.bfloat16)
+    w_b, w64 = rounded(rng, 2 * H * 128, 512, dtype=torch.bfloat16, s=0.05)
+    qa = torch.full((n, H, 576), -7.0, dtype=torch.bfloat16, device="cuda")
+    status.zero_()
+    tpc.tpc_latent_absorb(q, w_b, i32(kv), row_start=i32(start), qa=qa, status=status)
+    assert status.item() == 7
+    x = host(qa)
+    for t in range(n):
+        if not claims[t]:
+            assert (x[t] == -7).all(), t
+        elif len(claims[t]) == 1:
+            b = claims[t][0]
+            ref, mag = od.absorb(q64[t:t + 1], w64, [kv[b] - (start[b + 1] - start[b]) + t - start[b] + 1])
+            tol = UBF * np.abs(ref) + np.where(np.arange(576) < 512, 140 * U32, 2.0 ** -19) * mag
+            within(x[t:t + 1], ref, tol, t)
+
+
+def test_absorb_of_bad_row_starts_in_large_batches(tpc):
+    """One decreasing pair among 300 sequences of several tiles: every other row is as in the sound batch."""
+    import torch
+    rng = np.random.default_rng(3)
+    H, m = 5, rng.integers(0, 4, 300)
+    m[[40, 41, 200]] = [2, 1, 3]
+    start = starts(m)
+    n = int(start[-1]) + 5
+    kv = i32(rng.integers(5, 9000, 300))
+    q, _ = rounded(rng, n, H, 192, dtype=torch.bfloat16)
+    w_b, _ = rounded(rng, 2 * H * 128, 512, dtype=torch.bfloat16, s=0.05)
+    status, res = new_status(), []
+    bad = start.copy()
+    bad[41] += 10 ** 6  # sequence 40 leaves the rows, sequence 41 decreases
+    for s in (start, bad):
+        qa = torch.full((n, H, 576), -7.0, dtype=torch.bfloat16, device="cuda")
+        status.zero_()
+        tpc.tpc_latent_absorb(q, w_b, kv, row_start=i32(s), qa=qa, status=status)
+        res.append(qa)
+        assert status.item() == (0 if s is start else 7)
+    lost = np.zeros(n, bool)
+    lost[start[40]:start[42]] = True
+    assert torch.equal(res[0][dev(~lost)], res[1][dev(~lost)])
+    assert bool((res[1][dev(lost)] == -7).all()) and bool((res[1][n - 5:] == -7).all())

@@ -46,11 +46,33 @@ struct RowAt {
   int64_t pos;  // may be negative
 };
 
+// the rows first .. end - 1 of a sequence lie within 0 .. n_rows (a sequence whose rows do not has none)
+__device__ __forceinline__ bool rows_ok(const DecodeRows& r, int first, int end) {
+  return first >= 0 && end >= first && end <= r.n_rows;
+}
+
+// the sequence and position of row t, by the whole warp
 __device__ __forceinline__ RowAt row_at(const DecodeRows& r, int t) {
   if (!r.row_start) return {t, (int64_t)r.kv_len[t] - 1};
-  const int b = seq_of_row(r.row_start, r.n_seqs, t);
-  if (b >= r.n_seqs || t < r.row_start[b]) return {-1, 0};
+  auto owns = [&](int b) { return t >= r.row_start[b] && t < r.row_start[b + 1] && rows_ok(r, r.row_start[b], r.row_start[b + 1]); };
+  int b = seq_of_row(r.row_start, r.n_seqs, t);
+  if (b >= r.n_seqs) return {-1, 0};
+  if (!owns(b)) {  // no sequence's row, or the search was misled by a table that decreases somewhere
+    uint32_t found = 0;
+    const int lane = threadIdx.x & 31;
+    for (b = lane; !found && b - lane < r.n_seqs; b += 32) found = __ballot_sync(0xffffffffu, b < r.n_seqs && owns(b));
+    if (!found) return {-1, 0};
+    b = b - lane - 32 + __ffs(found) - 1;
+  }
   return {b, (int64_t)r.kv_len[b] - r.row_start[b + 1] + t};
+}
+
+// Whether a sequence of this thread's (every `of`-th from `at`) has rows outside 0 .. n_rows
+__device__ __forceinline__ bool bad_row_starts(const DecodeRows& r, int64_t at, int64_t of) {
+  bool bad = false;
+  if (r.row_start)
+    for (int64_t b = at; b < r.n_seqs; b += of) bad |= !rows_ok(r, r.row_start[b], r.row_start[b + 1]);
+  return bad;
 }
 
 // 10000^(-2 i / 64) / (2 pi), the turns per position of the rotary pair i, as powers of 10000^(-1 / 32) (their
@@ -236,6 +258,7 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendArg
   const int64_t t64 = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   if (t64 >= a.rows.n_rows) return;
   const int t = (int)t64;
+  if (a.status && bad_row_starts(a.rows, t64 * 32 + lane, 32ll * a.rows.n_rows)) set_status(a.status, kStatusCheck);
   const T* c = (const T*)a.c + (size_t)t * a.ld_c;
   const T* kr = (const T*)a.kr + (size_t)t * a.ld_kr;
   float l[2][8];  // loaded before the search for the row's place, which is a chain of loads itself

@@ -923,6 +923,7 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
   uint8_t* sm = hsm_raw + ((1024u - (smem_u32(hsm_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t x_full, x_empty, w_full[L::w_slots], w_empty[L::w_slots], acc_full[2], acc_empty[2];
   __shared__ uint32_t tslot;
+  __shared__ int sound;  // 0: a sequence's rows are not within 0 .. n_rows
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   constexpr int kOut = kLatDim / 128;  // output blocks of a (rows, head) pair
   const int64_t first = (int64_t)blockIdx.x * a.blocks;
@@ -936,6 +937,7 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
     return {pair % a.H, pair / a.H * 128, g % kOut * 128, j == 0 || g % kOut == 0};
   };
   if (tid == 0) {
+    sound = 1;
     prefetch_tensor_map(&tma_x);
     prefetch_tensor_map(&tma_w);
     for (int i = 0; i < L::w_slots; ++i) {
@@ -1024,10 +1026,16 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
     __syncwarp();
   } else {
     const int sp = w & 3;
-    int row0 = 0, row1 = a.rows.n_rows;  // rows that belong to a sequence
+    int row0 = 0, row1 = a.rows.n_rows;  // rows that belong to a sequence, if the table is sound
+    bool all_sound = true;
     if (a.rows.row_start) {
       row0 = a.rows.row_start[0];
       row1 = min(row1, a.rows.row_start[a.rows.n_seqs]);
+      // the writing warps look through the table together, while the first copies and MMAs run
+      if (bad_row_starts(a.rows, tid - 64, kAbsorbThreads - 64)) sound = 0;
+      asm volatile("bar.sync 1, %0;" ::"n"(kAbsorbThreads - 64) : "memory");
+      all_sound = sound != 0;
+      if (!all_sound && lane == 0) set_status(a.status, kStatusCheck);
     }
     // this CTA's share of the rotary parts: a row per warp and block, while copies and MMAs run
     int64_t rope = (int64_t)a.rows.n_rows * blockIdx.x / gridDim.x + w - 2;
@@ -1044,6 +1052,13 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
       const Block b = block(j);
       if (!__all_sync(0xffffffffu, wait(&acc_full[j & 1], (j >> 1) & 1))) break;
       fence_after_sync();
+      const int mine = b.t0 + 32 * sp + lane;  // rows of this warp that belong to a sequence
+      uint32_t owned = __ballot_sync(0xffffffffu, mine >= row0 && mine < row1);
+      if (!all_sound) {
+        owned = 0;
+        for (int i = 0; i < 32 && b.t0 + 32 * sp + i < a.rows.n_rows; ++i)
+          if (row_at(a.rows, b.t0 + 32 * sp + i).seq >= 0) owned |= 1u << i;
+      }
 #pragma unroll
       for (int c0 = half; c0 < half + 64; c0 += 32) {
         uint32_t r[32];
@@ -1056,7 +1071,7 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
 #pragma unroll
         for (int i = lane >> 2; i < 32; i += 8) {
           const int t = b.t0 + 32 * sp + i;
-          if (t >= row0 && t < row1)
+          if (owned >> i & 1)
             *reinterpret_cast<uint4*>(a.qa + ((size_t)t * a.H + b.h) * kLatWidth + b.n0 + c0 + (lane & 3) * 8) =
                 *reinterpret_cast<const uint4*>(out + i * L::out_ld + (lane & 3) * 16);
         }
