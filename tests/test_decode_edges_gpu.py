@@ -165,3 +165,100 @@ def test_absorb_of_bad_row_starts_in_large_batches(tpc):
     lost[start[40]:start[42]] = True
     assert torch.equal(res[0][dev(~lost)], res[1][dev(~lost)])
     assert bool((res[1][dev(lost)] == -7).all()) and bool((res[1][n - 5:] == -7).all())
+
+
+# ------------------------------------------------------------------------------------ contexts cut into pieces
+def test_capture_and_replay_with_cut_contexts(tpc):
+    """A captured append and attention (and its joining launch), replayed with lengths that move between one
+    tile, few pieces and more than 32 pieces, against the same calls outside a graph and the definition."""
+    import torch
+    rng = np.random.default_rng(51)
+    page, most = 64, 6100
+    per = -(-most // page)
+    lengths = [[1, 50, 128, 0, 7], [6000, 0, 0, 0, 0], [3000, 130, 0, 6100, 64], [129, 257, 600, 40, 5000], [0, 0, 0, 0, 0], [0, 0, 6100, 1, 0]]
+    for H in (16, 24, 40):  # 16, 32 and 64 columns a tile
+        table = rng.permutation(5 * per).reshape(5, per).astype(np.int32)
+        cache, _ = rounded(rng, 5 * per, page, 576, dtype=torch.bfloat16)
+        tab, scratch, status = i32(table), tpc.latent_attn_scratch(H), new_status()
+        buf = dict(kv=i32(lengths[0]), qa=rounded(rng, 5, H, 576, dtype=torch.bfloat16)[0], x=rounded(rng, 5, 576, dtype=torch.bfloat16)[0])
+
+        def call(b, ch, sc):
+            tpc.tpc_latent_append(ch, tab, b["kv"], b["x"][:, :512], b["x"][:, 512:], status=status)
+            return tpc.tpc_latent_attn(b["qa"], ch, tab, b["kv"], SCALE, scratch=sc, status=status)
+
+        twin = cache.clone()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            call(buf, twin, scratch)
+        torch.cuda.current_stream().wait_stream(side)
+        twin.copy_(cache)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = call(buf, cache, scratch)
+        for kv in lengths + lengths[::-1]:
+            new = dict(kv=i32(kv), qa=rounded(rng, 5, H, 576, dtype=torch.bfloat16)[0], x=rounded(rng, 5, 576, dtype=torch.bfloat16)[0])
+            for k in buf:
+                buf[k].copy_(new[k])
+            graph.replay()
+            want = call(new, twin, tpc.latent_attn_scratch(H))
+            assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(cache, twin), kv
+        del graph
+        q64 = host(buf["qa"])
+        ref, lref, oa, sa = od.attention(q64, host(cache), table, lengths[0], SCALE)
+        tol = UBF * np.abs(ref) + (2 * 640 * U32 * sa[..., None] + 2.0 ** -14 + 2.0 ** -16 + most * U32) * oa
+        within(host(outs[0]), ref, tol, "o")
+        assert status.item() == 0
+
+
+def test_attention_bad_tables_of_cut_contexts(tpc):
+    """Bad entries anywhere in a long context, and lengths beyond its table, among contexts that shares cut: the
+    status is set and the other sequences are right."""
+    import torch
+    rng = np.random.default_rng(52)
+    page, per, H, kv = 64, 40, 16, [2500, 2560, 700]
+    cache, c64 = rounded(rng, 3 * per, page, 576, dtype=torch.bfloat16)
+    qa, q64 = rounded(rng, 3, H, 576, dtype=torch.bfloat16)
+    table = rng.permutation(3 * per).reshape(3, per).astype(np.int32)
+    ref, lref, oa, sa = od.attention(q64, c64, table, kv, SCALE)
+    tol = UBF * np.abs(ref) + (2 * 640 * U32 * sa[..., None] + 2.0 ** -14 + 2.0 ** -16 + 2560 * U32) * oa
+    for at, entry, length in ((0, 3 * per, 2560), (17, -1, 2560), (39, 2 ** 31 - 1, 2560), (20, -2 ** 31, 2560), (0, table[1, 0], 2561),
+                              (0, table[1, 0], 2 ** 31 - 1)):
+        bad = table.copy()
+        bad[1, at] = entry
+        status = new_status()
+        o, lse = tpc.tpc_latent_attn(qa, cache, i32(bad), i32([kv[0], length, kv[2]]), SCALE, status=status)
+        assert status.item() == 7, (at, entry, length)
+        for b in (0, 2):
+            within(host(o)[b], ref[b], tol[b], "o")
+            within(host(lse)[b], lref[b], 640 * U32 * sa[b] + 2.0 ** -18 + 2560 * U32 + 4 * U32 * np.abs(lref[b]), "lse")
+
+
+@pytest.mark.parametrize("start", [[0, 2, 1, 3], [-4, 1, 2, 3], [0, 1, 2, 9], [2 ** 31 - 1, 0, 1, 3], [0, -2 ** 31 + 1, 2 ** 31 - 1, 3], [3, 2, 1, 0]])
+def test_attention_bad_row_starts_of_cut_contexts(tpc, start):
+    """Malformed row tables over long contexts: reported, rows of no sequence and the memory around the outputs
+    stay as they were, rows of one sound sequence are right."""
+    import torch
+    rng = np.random.default_rng(53)
+    page, per, H, n, kv = 64, 50, 40, 3, [3000, 2 ** 31 - 1, 129]
+    cache, c64 = rounded(rng, 3 * per, page, 576, dtype=torch.bfloat16)
+    qa, q64 = rounded(rng, n, H, 576, dtype=torch.bfloat16)
+    table = rng.permutation(3 * per).reshape(3, per).astype(np.int32)
+    o = torch.full((9, H, 512), -7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((9, H), -7.0, device="cuda")
+    status = new_status()
+    tpc.tpc_latent_attn(qa, cache, i32(table), i32(kv), SCALE, row_start=i32(start), o=o[3:6], lse=lse[3:6], status=status)
+    assert status.item() == 7
+    for t in (o, lse):
+        assert bool((t[:3] == -7).all()) and bool((t[6:] == -7).all())
+    good = [b for b in range(3) if 0 <= start[b] <= start[b + 1] <= n]
+    for t in range(n):
+        owner = [b for b in good if start[b] <= t < start[b + 1]]
+        if not owner:
+            assert bool((o[3 + t] == -7).all())
+        elif len(owner) == 1 and kv[owner[0]] <= per * page:
+            b = owner[0]
+            seen = kv[b] - (start[b + 1] - start[b]) + 1 + t - start[b]
+            ref, lref, oa, sa = od.attention(q64[t:t + 1], c64, table[b:b + 1], [seen], SCALE)
+            tol = UBF * np.abs(ref) + (2 * 640 * U32 * sa[..., None] + 2.0 ** -14 + 2.0 ** -16 + 3000 * U32) * oa
+            within(host(o)[3 + t:4 + t], ref, tol, "o")
