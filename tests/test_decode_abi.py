@@ -105,6 +105,21 @@ def test_attention_refusals(tpc):
     assert at(r=rows(tpc, 0, 0, kv=None), qa=None) == 0
 
 
+def test_empty_batches_need_no_block_table(tpc):
+    """A table of no sequence has no memory (an empty tensor's address is NULL)."""
+    L = tpc.lib()
+    ap = lambda c, r: L.tpc_latent_append(c, r, None, 512, None, 64, 1, None, None)
+    at = lambda c, r: L.tpc_latent_attn(c, r, 4, 0.1, None, None, None, None, 0, None, None)
+    for call in (ap, at):
+        for r in ((0, 0, None, None), (0, 0, A, None), (3, 0, A, None)):
+            assert call(cache(tpc, table=None), rows(tpc, *r)) == 0
+            assert call(cache(tpc, table=None, max_pages=0), rows(tpc, *r)) == 0
+            assert call(cache(tpc, data=None), rows(tpc, *r)) == NULL
+            assert call(cache(tpc, max_pages=-1), rows(tpc, *r)) == SHAPE
+        assert call(cache(tpc, table=None), rows(tpc, 0, 3, A)) == 0
+        assert call(cache(tpc, table=None), rows(tpc, 3, 3)) == NULL
+
+
 def test_wrappers_refuse_cpu_tensors(tpc):
     import torch
     z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t)

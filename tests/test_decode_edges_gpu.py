@@ -262,3 +262,37 @@ def test_attention_bad_row_starts_of_cut_contexts(tpc, start):
             ref, lref, oa, sa = od.attention(q64[t:t + 1], c64, table[b:b + 1], [seen], SCALE)
             tol = UBF * np.abs(ref) + (2 * 640 * U32 * sa[..., None] + 2.0 ** -14 + 2.0 ** -16 + 3000 * U32) * oa
             within(host(o)[3 + t:4 + t], ref, tol, "o")
+
+
+# ------------------------------------------------------------------------------------ nothing to do
+@pytest.mark.parametrize("seqs", [0, 3])
+def test_empty_batches(tpc, seqs):
+    """No live sequence, and sequences without a new row: every call returns its empty result and touches nothing."""
+    import torch
+    z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t, device="cuda")
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    H, status = 2, new_status()
+    for start in ([None] if seqs == 0 else []) + [i(seqs + 1)]:
+        cache = z(4, 16, 576) + 3
+        kw = dict(row_start=start, status=status)
+        tpc.tpc_latent_append(cache, i(seqs, 2), i(seqs), z(0, 512), z(0, 64), **kw)
+        assert bool((cache == 3).all())
+        assert tpc.tpc_latent_absorb(z(0, H, 192), z(512, 512), i(seqs), **kw).shape == (0, H, 576)
+        o, lse = tpc.tpc_latent_attn(z(0, H, 576), cache, i(seqs, 2), i(seqs), SCALE, **kw)
+        assert o.shape == (0, H, 512) and lse.shape == (0, H)
+        assert tpc.tpc_latent_expand(z(0, H, 512), z(512, 512), status=status).shape == (0, H, 128)
+        x, state = z(0, H, 64), z(4, H, 64, 64, t=torch.float32) + 3
+        src = torch.arange(seqs, dtype=torch.int32, device="cuda")
+        assert tpc.tpc_kda_step(state, src, x, x, x, x, z(0, H), **kw).shape == (0, H, 64)
+        assert bool((state == 3).all())
+    # rows that belong to no sequence
+    n = 2
+    cache, start = z(4, 16, 576) + 3, i(1)
+    qa, o = z(n, H, 576) + 3, z(n, H, 512) + 3
+    lse = z(n, H, t=torch.float32) + 3
+    tpc.tpc_latent_append(cache, i(0, 2), i(0), z(n, 512), z(n, 64), row_start=start, status=status)
+    tpc.tpc_latent_absorb(z(n, H, 192), z(512, 512), i(0), row_start=start, qa=qa, status=status)
+    tpc.tpc_latent_attn(z(n, H, 576), cache, i(0, 2), i(0), SCALE, row_start=start, o=o, lse=lse, status=status)
+    for t in (cache, qa, o, lse):
+        assert bool((t == 3).all())
+    assert status.item() == 0

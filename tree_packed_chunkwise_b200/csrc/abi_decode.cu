@@ -37,9 +37,12 @@ int rows_check(const char* call, const tpc_rows* r, bool kv, tpc::DecodeRows* ou
   return TPC_OK;
 }
 
-int cache_check(const char* call, const tpc_latent_cache* c, tpc::LatentCache* out) {
-  if (!c || !c->data || !c->block_table) return fail(TPC_ERR_NULL, std::string(call) + ": cache, its data or its block table is NULL");
-  if (c->n_pages < 1 || c->max_pages < 1) return fail(TPC_ERR_BAD_SHAPE, std::string(call) + ": n_pages and max_pages must be >= 1");
+// (a batch without a row or a sequence reads no table)
+int cache_check(const char* call, const tpc_latent_cache* c, bool empty, tpc::LatentCache* out) {
+  if (!c || !c->data || (!empty && !c->block_table))
+    return fail(TPC_ERR_NULL, std::string(call) + ": cache, its data or its block table is NULL");
+  if (c->n_pages < 1 || c->max_pages < (empty ? 0 : 1))
+    return fail(TPC_ERR_BAD_SHAPE, std::string(call) + ": n_pages and max_pages must be >= 1");
   if (!(c->page_size == 16 || c->page_size == 32 || (c->page_size >= 64 && c->page_size % 64 == 0)))
     return fail(TPC_ERR_UNSUPPORTED, std::string(call) + ": page_size must be 16, 32 or a multiple of 64");
   // (room for a tile past the end)
@@ -103,10 +106,11 @@ int tpc_latent_append(const tpc_latent_cache* cache, const tpc_rows* rows, const
                       int64_t ld_kr, int32_t in_dtype, int32_t* status, tpc_stream_t stream) {
   tpc::LatentCache lc;
   tpc::DecodeRows r;
-  if (int rc = cache_check("latent append", cache, &lc)) return rc;
   if (int rc = rows_check("latent append", rows, true, &r)) return rc;
+  const bool empty = r.n_rows == 0 || r.n_seqs == 0;
+  if (int rc = cache_check("latent append", cache, empty, &lc)) return rc;
   if (in_dtype != TPC_F32 && in_dtype != TPC_BF16) return fail(TPC_ERR_UNSUPPORTED, "latent append: in_dtype is TPC_F32 or TPC_BF16");
-  if (r.n_rows == 0 || r.n_seqs == 0) return TPC_OK;
+  if (empty) return TPC_OK;
   if (!c || !kr) return fail(TPC_ERR_NULL, "latent append: NULL tensor");
   const int unit = in_dtype == TPC_BF16 ? 8 : 4;
   if (ld_c < tpc::kLatDim || ld_kr < tpc::kLatRope || ld_c % unit || ld_kr % unit || misaligned(c) || misaligned(kr))
@@ -155,10 +159,11 @@ int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t
                     void* o, float* lse, void* scratch, size_t scratch_bytes, int32_t* status, tpc_stream_t stream) {
   tpc::LatentCache lc;
   tpc::DecodeRows r;
-  if (int rc = cache_check("latent attention", cache, &lc)) return rc;
   if (int rc = rows_check("latent attention", rows, true, &r)) return rc;
+  const bool empty = r.n_rows == 0 || r.n_seqs == 0;
+  if (int rc = cache_check("latent attention", cache, empty, &lc)) return rc;
   if (int rc = heads_check("latent attention", H, r.n_rows)) return rc;
-  if (r.n_rows == 0 || r.n_seqs == 0) return TPC_OK;
+  if (empty) return TPC_OK;
   if (!qa || !o || !lse || !scratch) return fail(TPC_ERR_NULL, "latent attention: NULL tensor");
   if (misaligned(qa) || misaligned(o)) return fail(TPC_ERR_BAD_SHAPE, "latent attention: qa and o must be 16-byte aligned");
   if (scratch_bytes < tpc_latent_attn_scratch_bytes(H) || misaligned(scratch, 256))
