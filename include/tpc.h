@@ -691,6 +691,13 @@ long long tpc_launch_count(void);
  * TPC_ERR_TIMEOUT into *status (a caller-owned device int) and returns; the context stays usable.
  */
 int tpc_debug_wait_timeout(int32_t* status, int64_t timeout_ns, tpc_stream_t stream);
+/*
+ * Limit (ns, at most 2e9, the default) of the waits in the tensor-core kernels of token-by-token
+ * generation that later calls of the process launch; returns the former limit, and sets none if ns is
+ * negative.  With 0 every wait gives up at once, for tests of the ways out: the call then records
+ * TPC_ERR_TIMEOUT and its outputs are unspecified.
+ */
+int64_t tpc_debug_wait_limit(int64_t ns);
 
 /* ------------------------------------------------------------------ index and bounds mode */
 /*

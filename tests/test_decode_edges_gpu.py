@@ -296,3 +296,61 @@ def test_empty_batches(tpc, seqs):
     for t in (cache, qa, o, lse):
         assert bool((t == 3).all())
     assert status.item() == 0
+
+
+# ------------------------------------------------------------------------------------ waits that run out
+def test_waits_that_run_out_leave_the_device_usable(tpc):
+    """With a limit of zero every tensor-core kernel gives up at its first wait, with copies and perhaps products in
+    flight: it records the timeout, writes nothing outside its outputs, and the next calls are right."""
+    import torch
+    rng = np.random.default_rng(61)
+    guard = 4096
+
+    def framed(*s, t=torch.bfloat16):
+        """A tensor inside a larger one, and the larger one."""
+        n = int(np.prod(s))
+        whole = torch.full((n + 2 * guard,), -7.0, dtype=t, device="cuda")
+        return whole[guard:guard + n].view(*s), whole
+
+    def untouched(whole):
+        return bool((whole[:guard] == -7).all()) and bool((whole[-guard:] == -7).all())
+
+    calls = []
+    for H, m, kv in ((16, 1, 20000), (16, 2, 5000), (16, 40, 3000), (5, 3, 100), (40, 1, 64)):
+        B = 6
+        table, n_pages = batch(rng, [kv] * B, 64)
+        cache, _ = rounded(rng, n_pages, 64, 576, dtype=torch.bfloat16)
+        qa, _ = rounded(rng, B * m, H, 576, dtype=torch.bfloat16)
+        args = (qa, cache, i32(table), i32([kv] * B), SCALE)
+        start = i32(np.arange(B + 1) * m)
+        calls.append(([((B * m, H, 512), torch.bfloat16), ((B * m, H), torch.float32)],
+                      lambda out, st, args=args, start=start: tpc.tpc_latent_attn(*args, row_start=start, o=out[0], lse=out[1], status=st)))
+    for n, H in ((1, 16), (500, 16), (3000, 16), (130, 3)):
+        q, _ = rounded(rng, n, H, 192, dtype=torch.bfloat16)
+        o, _ = rounded(rng, n, H, 512, dtype=torch.bfloat16)
+        w_b, _ = rounded(rng, 2 * H * 128, 512, dtype=torch.bfloat16, s=0.05)
+        kv = i32(rng.integers(1, 9000, n))
+        calls.append(([((n, H, 576), torch.bfloat16)], lambda out, st, a=(q, w_b, kv): tpc.tpc_latent_absorb(*a, qa=out[0], status=st)))
+        calls.append(([((n, H, 128), torch.bfloat16)], lambda out, st, a=(o, w_b): tpc.tpc_latent_expand(*a, out=out[0], status=st)))
+
+    def run(code):
+        res = []
+        for shapes, call in calls:
+            frames, status = [framed(*s, t=t) for s, t in shapes], new_status()
+            call([f[0] for f in frames], status)
+            torch.cuda.synchronize()
+            assert status.item() == code and all(untouched(f[1]) for f in frames)
+            res.append([f[0] for f in frames])
+        return res
+
+    before = run(0)
+    normal = tpc.tpc_debug_wait_limit(0)
+    try:
+        run(8)
+        run(8)
+    finally:
+        assert tpc.tpc_debug_wait_limit(normal) == 0
+    assert normal == 2_000_000_000
+    after = run(0)
+    for a, b in zip(before, after):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))

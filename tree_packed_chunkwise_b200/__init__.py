@@ -179,6 +179,7 @@ SIGNATURES = {
     "tpc_profile_read": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_size_t]),
     "tpc_launch_count": (ctypes.c_longlong, []),
     "tpc_debug_wait_timeout": (ctypes.c_int, [_V, ctypes.c_int64, _V]),
+    "tpc_debug_wait_limit": (ctypes.c_int64, [ctypes.c_int64]),
     "tpc_checks_enable": (None, [ctypes.c_int]),
     "tpc_checks_enabled": (ctypes.c_int, []),
     "tpc_plan_check_device": (ctypes.c_int, [_V, _V]),
@@ -579,6 +580,11 @@ def tpc_debug_wait_timeout(status, timeout_ns=1_000_000, stream=None):
     """Runs the library's bounded device wait on a barrier nothing arrives on; status (int32 device
     tensor) receives TPC_ERR_TIMEOUT."""
     _check(lib().tpc_debug_wait_timeout(_ptr(status), int(timeout_ns), _stream_ptr(stream)))
+
+
+def tpc_debug_wait_limit(ns=-1) -> int:
+    """Sets the limit (ns) of the waits in later calls' generation kernels; returns the former one (negative: only that)."""
+    return int(lib().tpc_debug_wait_limit(int(ns)))
 
 
 # ------------------------------------------------------------------------------------ dense products

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <string>
 
 #include "../../include/tpc.h"
@@ -24,6 +25,8 @@ static_assert(TPC_LATENT_DIM == tpc::kLatDim && TPC_LATENT_ROPE == tpc::kLatRope
               "cache layout");
 
 constexpr int kLatMaxH = 128;
+
+std::atomic<int64_t> g_wait_ns{2000000000};  // limit of the tensor-core kernels' waits
 
 bool misaligned(const void* p, size_t to = 16) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 
@@ -146,7 +149,7 @@ int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld
   const int64_t total = (int64_t)((r.n_rows + 127) / 128) * H * (tpc::kLatDim / 128);
   const int64_t slots = (int64_t)tpc::kAbsorbPerSm * tpc_abi::sm_count(), blocks = (total + slots - 1) / slots;
   const int64_t grid = (total + blocks - 1) / blocks;
-  const tpc::AbsorbArgs a{r, H, (const bf*)q, ld_q, (bf*)qa, status, total, (int)blocks};
+  const tpc::AbsorbArgs a{r, H, (const bf*)q, ld_q, (bf*)qa, status, (uint64_t)g_wait_ns, total, (int)blocks};
   constexpr size_t smem = tpc::AbsorbSmem::total;
   TPC_CUDA(set_smem(tpc::latent_absorb_tc, smem));
   TPC_LAUNCH("latent_absorb_tc", st, (tpc::latent_absorb_tc<<<(unsigned)grid, tpc::kAbsorbThreads, smem, st>>>(tx, tw, a)));
@@ -179,7 +182,7 @@ int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t
     return fail(TPC_ERR_CUDA, "latent attention: cuTensorMapEncodeTiled failed");
   char* sc = static_cast<char*>(scratch);
   const tpc::LatAttnArgs a{lc, r, H, scale * 1.4426950408889634f, (bf*)o, lse, (float*)sc, (float2*)(sc + tpc::kLatPartBytes),
-                           (tpc::LatPiece*)(sc + tpc::kLatPartBytes + tpc::kLatMlBytes), status};
+                           (tpc::LatPiece*)(sc + tpc::kLatPartBytes + tpc::kLatMlBytes), status, (uint64_t)g_wait_ns};
   const int grid = std::min(tpc_abi::sm_count(), tpc::kLatMaxCtas);
   auto go = [&](auto nt) -> int {
     constexpr int N = decltype(nt)::value;
@@ -214,7 +217,7 @@ int tpc_latent_expand(int32_t n_rows, int32_t H, const void* o, const void* w_b,
   if (misaligned(o) || misaligned(w_b) || misaligned(out)) return fail(TPC_ERR_BAD_SHAPE, "latent expand: tensors must be 16-byte aligned");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   tpc_abi::NvtxRange nvtx_call("tpc_latent_expand");
-  const tpc::ExpandArgs a{H, n_rows, (bf*)out, status};
+  const tpc::ExpandArgs a{H, n_rows, (bf*)out, status, (uint64_t)g_wait_ns};
   const int64_t pairs = (int64_t)((n_rows + 127) / 128) * H;
   auto go = [&](auto bn) -> int {
     constexpr int BN = decltype(bn)::value;
@@ -232,5 +235,7 @@ int tpc_latent_expand(int32_t n_rows, int32_t H, const void* o, const void* w_b,
   if (pairs * (tpc::kLatHead / 32) <= 2 * tpc_abi::sm_count()) return go(std::integral_constant<int, 32>{});
   return go(std::integral_constant<int, 128>{});
 }
+
+int64_t tpc_debug_wait_limit(int64_t ns) { return ns < 0 ? g_wait_ns.load() : g_wait_ns.exchange(std::min<int64_t>(ns, 2000000000)); }
 
 }  // extern "C"

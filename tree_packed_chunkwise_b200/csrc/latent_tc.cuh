@@ -59,6 +59,14 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The kernels' waits are bounded by a limit of their arguments; with 0 they give up at once, so that the ways
+// out can be tested (the attention, whose waits cost time, starts as if one had run out).  What a CTA waits for on its way out (its copies to land, its MMAs to complete) is
+// bounded by kWayOutNs instead, whatever the limit.
+constexpr uint64_t kWayOutNs = 2000000000ull;
+__device__ __forceinline__ bool mbar_wait_limit(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  return limit_ns ? mbar_wait(bar, parity, limit_ns) : mbar_test_wait(bar, parity);
+}
+
 // fetches a tensor map (a __grid_constant__ parameter) ahead of its first use
 __device__ __forceinline__ void prefetch_tensor_map(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
@@ -121,6 +129,7 @@ struct LatAttnArgs {
   float2* ml;
   LatPiece* meta;
   int* status;
+  uint64_t wait_ns;
 };
 
 struct LatSeq {
@@ -335,7 +344,8 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       mbar_init(&o_done[i], 1);
     }
     for (uint64_t* b : {q_full, q_empty, done}) mbar_init(b, 1);
-    *abort_flag = 0;
+    *abort_flag = a.wait_ns == 0;
+    if (a.wait_ns == 0) set_status(a.status, 8);
     where->b = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -368,15 +378,15 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
   const uint32_t tb = *tslot;
   LatWalk<NT> walk(a, *where, where->b < 0 ? 0 : share);  // (< 0: the lengths changed under the call)
   auto aborted = [&] { return *((volatile int*)abort_flag) != 0; };
-  // Every wait is bounded.  After the first that runs out no role waits, copies or multiplies any
-  // more, but all walk on to the end of their loops, so the barriers between the softmax warps match.
+  // Every wait is bounded.  After the first that runs out no role waits any more; the producer stops, the
+  // others walk on to the end of their loops, so the barriers between the softmax warps match.
   auto give_up = [&] {
     set_status(a.status, 8);
     atomicExch(abort_flag, 1);
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (aborted()) return false;
-    if (mbar_wait(bar, parity, 2000000000ull)) return true;
+    if (mbar_wait(bar, parity, a.wait_ns)) return true;
     give_up();
     return false;
   };
@@ -405,28 +415,30 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       }
       return t;
     };
-    int it = 0, piece = -1;
+    int it = 0, pieces = 0, ring_sent = 0, rope_sent = 0;  // tiles, and copies issued to each kind of slot
+    bool ok = true;
     Tile cur = fetch(), nxt = cur;
-    while (cur.valid) {
+    while (cur.valid && ok) {
       if (cur.page < 0 || cur.page >= a.cache.n_pages) {
         set_status(a.status, kStatusCheck);
         cur.page = 0;
       }
       const int my_row = cur.page * ps + cur.off;
       if (cur.first) {
-        ++piece;
-        if (__all_sync(0xffffffffu, piece == 0 || wait(q_empty, (piece - 1) & 1))) {
-          if (lane == 0) mbar_arrive_expect_tx(q_full, kLatChunks * NT * 128);
-          __syncwarp();
-          if (lane < kLatChunks) tma_load_2d(sm + L::q + lane * NT * 128, &tma_q, 64 * lane, cur.q_row, q_full);
-        }
+        ok = __all_sync(0xffffffffu, pieces == 0 || wait(q_empty, (pieces - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(q_full, kLatChunks * NT * 128);
+        __syncwarp();
+        if (lane < kLatChunks) tma_load_2d(sm + L::q + lane * NT * 128, &tma_q, 64 * lane, cur.q_row, q_full);
+        ++pieces;
       }
       for (int e = 0; e < kLatItems; ++e) {
         const uint32_t st = L::slot_of(it, e), uses = L::uses_of(it, e);
         const int nc = e == 0 ? 1 : 2;  // chunks of the item: 8, then 0 1, 2 3, 4 5, 6 7
         if (e == 1) nxt = fetch();
-        const bool ok = uses == 0 || wait(&empty[st], (uses - 1) & 1);
-        if (!__all_sync(0xffffffffu, ok)) continue;
+        ok = __all_sync(0xffffffffu, uses == 0 || wait(&empty[st], (uses - 1) & 1));
+        if (!ok) break;
+        ++(L::own_rope && e == 0 ? rope_sent : ring_sent);
         if (lane == 0) {
           if (cur.segs)
             mbar_arrive_expect_tx(&full[st], cur.segs * nc * box * 128);
@@ -443,10 +455,10 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       cur = nxt;
       ++it;
     }
-    if (aborted() && lane == 0) {  // copies in flight land before the CTA ends
-      for (int i = max(0, it * L::ring_items - U); i < it * L::ring_items; ++i) mbar_wait(&full[i % U], (i / U) & 1, 100000000ull);
-      if (L::own_rope && it > 0) mbar_wait(&full[U], (it - 1) & 1, 100000000ull);
-      if (piece >= 0) mbar_wait(q_full, piece & 1, 100000000ull);
+    if (lane == 0) {  // every copy lands before the CTA ends, whoever gave up (at once if no one did)
+      for (int i = max(0, ring_sent - U); i < ring_sent; ++i) mbar_wait(&full[i % U], (i / U) & 1, kWayOutNs);
+      if (rope_sent > 0) mbar_wait(&full[U], (rope_sent - 1) & 1, kWayOutNs);
+      if (pieces > 0) mbar_wait(q_full, (pieces - 1) & 1, kWayOutNs);
     }
   } else if (w == 1) {  // ---- MMA
     // The whole warp walks the loops and one elected lane issues, so that descriptors stay in uniform
@@ -509,7 +521,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
         if (__any_sync(0xffffffffu, aborted())) return false;
         const uint64_t t = globaltimer();
         if (t0 == 0) t0 = t;
-        if (t - t0 > 2000000000ull) give_up();
+        if (t - t0 > a.wait_ns) give_up();
       }
       return true;
     };
@@ -551,8 +563,8 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
       }
     }
     sum_now();
-    commit_if(lead, done);
-    if (!mbar_wait(done, 0, 2000000000ull)) set_status(a.status, 8);
+    commit_if(lead, done);  // the MMAs are complete before TMEM is freed, whoever gave up
+    if (!mbar_wait(done, 0, kWayOutNs)) set_status(a.status, 8);
     __syncwarp();
   } else {  // ---- softmax warps: sub-partition sp holds tokens 16 G sp .. 16 G sp + 16 G - 1 of a tile, and
             //      latent dimensions 32 sp .. 32 sp + 31 of each 128-row block of O^T
@@ -911,6 +923,7 @@ struct AbsorbArgs {
   int64_t ld_q;
   __nv_bfloat16* qa;
   int* status;
+  uint64_t wait_ns;
   int64_t total;  // blocks in all, and of one CTA
   int blocks;
 };
@@ -921,7 +934,7 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
   using L = AbsorbSmem;
   extern __shared__ __align__(1024) uint8_t hsm_raw[];
   uint8_t* sm = hsm_raw + ((1024u - (smem_u32(hsm_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t x_full, x_empty, w_full[L::w_slots], w_empty[L::w_slots], acc_full[2], acc_empty[2];
+  __shared__ __align__(8) uint64_t x_full, x_empty, w_full[L::w_slots], w_empty[L::w_slots], acc_full[2], acc_empty[2], done;
   __shared__ uint32_t tslot;
   __shared__ int sound;  // 0: a sequence's rows are not within 0 .. n_rows
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
@@ -946,6 +959,7 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
     }
     mbar_init(&x_full, 1);
     mbar_init(&x_empty, 1);
+    mbar_init(&done, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 8);
@@ -959,7 +973,7 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
   const uint32_t tb = tslot;
   // every wait is bounded; a role whose wait ran out records it and stops
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_wait(bar, parity, 2000000000ull)) return true;
+    if (mbar_wait_limit(bar, parity, a.wait_ns)) return true;
     set_status(a.status, 8);
     return false;
   };
@@ -987,10 +1001,9 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
           tma_load_2d(ws + L::w / 2, &tma_w, b.n0 + 64, b.h * kLatHead + 64 * kc, &w_full[st]);
         }
       }
-      if (!ok) {  // copies in flight land before the CTA ends
-        for (int i = max(0, item - L::w_slots); i < item; ++i) mbar_wait(&w_full[i % L::w_slots], (i / L::w_slots) & 1, 100000000ull);
-        if (xs) mbar_wait(&x_full, (xs - 1) & 1, 100000000ull);
-      }
+      // every copy lands before the CTA ends, whoever gave up (at once if no one did)
+      for (int i = max(0, item - L::w_slots); i < item; ++i) mbar_wait(&w_full[i % L::w_slots], (i / L::w_slots) & 1, kWayOutNs);
+      if (xs) mbar_wait(&x_full, (xs - 1) & 1, kWayOutNs);
     }
   } else if (w == 1) {
     const uint32_t lead = elect_one();
@@ -1021,8 +1034,8 @@ __global__ void __launch_bounds__(kAbsorbThreads, kAbsorbPerSm)
       commit_if(lead, &acc_full[j & 1]);
       if (leaves) commit_if(lead, &x_empty);
     }
-    // the last MMAs are complete before TMEM is freed
-    if (ok && count > 0) wait(&acc_full[(count - 1) & 1], ((count - 1) >> 1) & 1);
+    commit_if(lead, &done);  // the MMAs are complete before TMEM is freed, whoever gave up
+    if (!mbar_wait(&done, 0, kWayOutNs)) set_status(a.status, 8);
     __syncwarp();
   } else {
     const int sp = w & 3;
@@ -1106,6 +1119,7 @@ struct ExpandArgs {
   int H, n_rows;
   __nv_bfloat16* out;
   int* status;
+  uint64_t wait_ns;
 };
 
 template <int BN>
@@ -1115,7 +1129,7 @@ __global__ void __launch_bounds__(kExpandThreads)
   using L = ExpandSmem<BN>;
   extern __shared__ __align__(1024) uint8_t hsm_raw[];
   uint8_t* sm = hsm_raw + ((1024u - (smem_u32(hsm_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t full[L::stages], empty[L::stages], acc_full;
+  __shared__ __align__(8) uint64_t full[L::stages], empty[L::stages], acc_full, done;
   __shared__ uint32_t tslot;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int n0 = (int)(blockIdx.x % (kLatHead / BN)) * BN, pair = (int)(blockIdx.x / (kLatHead / BN));
@@ -1128,6 +1142,7 @@ __global__ void __launch_bounds__(kExpandThreads)
       mbar_init(&empty[i], 1);
     }
     mbar_init(&acc_full, 1);
+    mbar_init(&done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (w == 1) tmem_alloc(&tslot, BN);
@@ -1137,7 +1152,7 @@ __global__ void __launch_bounds__(kExpandThreads)
   const uint32_t tb = tslot;
   // every wait is bounded; a role whose wait ran out records it and stops
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_wait(bar, parity, 2000000000ull)) return true;
+    if (mbar_wait_limit(bar, parity, a.wait_ns)) return true;
     set_status(a.status, 8);
     return false;
   };
@@ -1152,8 +1167,8 @@ __global__ void __launch_bounds__(kExpandThreads)
         tma_load_3d(xs, &tma_x, k0, h, t0, &full[st]);
         tma_load_2d(xs + L::x, &tma_w, k0, (a.H + h) * kLatHead + n0, &full[st]);
       }
-      if (issued < L::steps)  // copies in flight land before the CTA ends
-        for (int i = max(0, issued - L::stages); i < issued; ++i) mbar_wait(&full[i % L::stages], (i / L::stages) & 1, 100000000ull);
+      // every copy lands before the CTA ends, whoever gave up (at once if no one did)
+      for (int i = max(0, issued - L::stages); i < issued; ++i) mbar_wait(&full[i % L::stages], (i / L::stages) & 1, kWayOutNs);
     }
   } else if (w == 1) {
     const uint32_t lead = elect_one();
@@ -1170,10 +1185,9 @@ __global__ void __launch_bounds__(kExpandThreads)
       for (int ks = 0; ks < 4; ++ks) mma_bf16_if(lead, tb, sw_desc_k(xs, 128, ks), sw_desc_k(xs + L::x, BN, ks), id, i || ks ? 1u : 0u);
       commit_if(lead, &empty[st]);
     }
-    // also after a wait that ran out: the MMAs issued so far are complete before TMEM is freed, but then
-    // the epilogue must not take the accumulator for whole
-    if (ok) commit_if(lead, &acc_full);
-    if (ok) wait(&acc_full, 0);
+    if (ok) commit_if(lead, &acc_full);  // (otherwise the accumulator is not whole)
+    commit_if(lead, &done);              // the MMAs are complete before TMEM is freed, whoever gave up
+    if (!mbar_wait(&done, 0, kWayOutNs)) set_status(a.status, 8);
     __syncwarp();
   } else {
     const int sp = w & 3;
