@@ -620,9 +620,9 @@ int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld
  * first): row at position p reads cached tokens 0 .. p of its sequence,
  *   o[t][h] = sum_j softmax_j(scale qa[t][h] . cache_j) c_j   (bf16 [n_rows][H][512]),
  *   lse[t][h] = log sum_j exp(scale qa[t][h] . cache_j)        (fp32 [n_rows][H], natural log).
- * A row without a token gets o = 0 and lse = -infinity.  Tokens past kv_len are never used,
- * whatever the page holds there; a latent that is not finite among the kv_len tokens can make any row
- * of its sequence NaN, rows before it included.  Scores, softmax statistics and sums in fp32; a
+ * A row without a token gets o = 0 and lse = -infinity.  Tokens past a row's position, and
+ * past kv_len, are never used, whatever the cache holds there; rows that see a latent that is not finite
+ * are not finite.  Scores, softmax statistics and sums in fp32; a
  * weight enters its product as two bf16 values, off by less than 2^-16 of itself.  qa: [n_rows][H][576] bf16,
  * 16-byte aligned, 1 <= H <= 128.
  *   scratch: tpc_latent_attn_scratch_bytes(H) bytes, 256-byte aligned, used by one call at a time.

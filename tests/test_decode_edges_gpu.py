@@ -354,3 +354,49 @@ def test_waits_that_run_out_leave_the_device_usable(tpc):
     after = run(0)
     for a, b in zip(before, after):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# ------------------------------------------------------------------------------------ values that are not finite
+@pytest.mark.parametrize("H,m", [(5, 3), (16, 2), (16, 3), (16, 4), (16, 9), (3, 70), (40, 150)])
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+def test_attention_does_not_see_later_tokens(tpc, H, m, value):
+    """A later token of the same run that is not finite (in one dimension, in all, in its rotary key) leaves the
+    rows before it as they are; a query that is not finite leaves the other rows as they are."""
+    import torch
+    rng = np.random.default_rng(7 * H + m)
+    page, kv = 64, 300
+    table = rng.permutation(5).astype(np.int32)[None]
+    clean, _ = rounded(rng, 5, page, 576, dtype=torch.bfloat16)
+    qa, _ = rounded(rng, m, H, 576, dtype=torch.bfloat16)
+    start, bad = i32([0, m]), float(value)
+
+    def call(cache, q):
+        status = new_status()
+        o, lse = tpc.tpc_latent_attn(q, cache, i32(table), i32([kv]), SCALE, row_start=start, status=status)
+        assert status.item() == 0
+        return o, lse
+
+    def token(cache, j):
+        return cache[int(table[0, j // page]), j % page]
+
+    o0, l0 = call(clean, qa)
+    assert bool(torch.isfinite(o0.float()).all())
+    for row in {1, m // 2, m - 1}:       # the row at kv - m + row and all behind it see the token
+        for dims in (slice(0, 512), slice(37, 38), slice(511, 512), slice(540, 541), slice(0, 576)):
+            cache = clean.clone()
+            token(cache, kv - m + row)[dims] = bad
+            o, lse = call(cache, qa)
+            assert torch.equal(o[:row], o0[:row]) and torch.equal(lse[:row], l0[:row]), (row, dims)
+            if dims.stop - dims.start > 64 and value == "nan":
+                assert bool(torch.isnan(o[row:].float()).all()) and bool(torch.isnan(lse[row:]).all())
+    cache = clean.clone()                # several of them
+    for j in range(kv - m + 1, kv):
+        token(cache, j)[j % 512] = bad
+    o, lse = call(cache, qa)
+    assert torch.equal(o[0], o0[0]) and torch.equal(lse[0], l0[0])
+    for row in {0, m // 2, m - 1}:       # a query: the other rows' tokens stay in their sums
+        q = qa.clone()
+        q[row, :, 5] = bad
+        o, lse = call(clean, q)
+        rest = torch.arange(m, device="cuda") != row
+        assert torch.equal(o[rest], o0[rest]) and torch.equal(lse[rest], l0[rest]), row

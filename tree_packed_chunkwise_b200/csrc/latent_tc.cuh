@@ -597,6 +597,45 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
 #pragma unroll
         for (int g = 0; g < G; ++g) tmem_ld_16x256<R>(la + ((uint32_t)(16 * g) << 16) + kScores + (it & 1) * NT, x[g]);
         const bool mask = t0 + KT - 1 > lim0;
+        // Tokens of the tile that some of the rows do not see: with a weight of 0 a latent that is not finite would
+        // still make their sums NaN.  Its scores are not finite either, so only then the latents are looked
+        // at, those that are not finite leave the product, and the rows that see them become NaN here.
+        const int part0 = max(max(lim0 + 1 - t0, 0), 16 * G * sp), part1 = min(min(s.kv - t0, KT), 16 * G * (sp + 1));
+        if (part0 < part1) {  // (of this warp's tokens)
+          bool odd = false;
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int j = 0; j < 4 * R; ++j) odd |= !(fabsf(x[g][j]) <= 3.4028235e38f);
+          if (__any_sync(0xffffffffu, odd)) {
+            uint32_t gone = 0;
+#pragma unroll 1
+            for (int r = part0; r < part1; ++r) {
+              uint4 v[2];
+              bool bad = false;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {  // 16-byte unit lane + 32 h of the row: chunk 4 h + lane / 8
+                const int c = 4 * h + (lane >> 3);
+                uint8_t* p = sm + L::ring + L::slot_of(it, 1 + (c >> 1)) * L::slot + (c & 1) * L::chunk + r * 128 + (lane & 7) * 16;
+                v[h] = *reinterpret_cast<const uint4*>(p);
+                for (uint32_t u : {v[h].x, v[h].y, v[h].z, v[h].w}) bad |= (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+              }
+              if (!__any_sync(0xffffffffu, bad)) continue;
+              gone |= 1u << (r - 16 * G * sp);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int c = 4 * h + (lane >> 3);
+                uint8_t* p = sm + L::ring + L::slot_of(it, 1 + (c >> 1)) * L::slot + (c & 1) * L::chunk + r * 128 + (lane & 7) * 16;
+                *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+              }
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+              for (int j = 0; j < 4 * R; ++j)
+                if (gone >> (16 * g + 8 * (j >> 1 & 1) + (lane >> 2)) & 1) x[g][j] = __int_as_float(0x7fffffff);
+          }
+        }
         float tm[2 * R];
 #pragma unroll
         for (int c = 0; c < 2 * R; ++c) {  // maximum of each column over the tile
