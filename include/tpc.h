@@ -598,8 +598,8 @@ typedef struct tpc_latent_cache {
  *   may be slices of a projection.
  * Rows without a token are skipped.  Two rows that write one cached token (a page of two
  * sequences that both write it) race: with a status word that records TPC_ERR_DEVICE_CHECK (a
- * comparison of every written page with every other one of the batch: 1 us at 100 single tokens, 16 us
- * at 4096).
+ * comparison of every written page with every other one of the batch: 1 us at 100 single tokens, 14 us
+ * at 4096, 54 us if they are given by row_start; 15 us at a run of 100,000 tokens in 16-token pages).
  */
 int tpc_latent_append(const tpc_latent_cache* cache, const tpc_rows* rows, const void* c, int64_t ld_c,
                       const void* kr, int64_t ld_kr, int32_t in_dtype, int32_t* status, tpc_stream_t stream);

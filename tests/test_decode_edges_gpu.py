@@ -400,3 +400,70 @@ def test_attention_does_not_see_later_tokens(tpc, H, m, value):
         o, lse = call(clean, q)
         rest = torch.arange(m, device="cuda") != row
         assert torch.equal(o[rest], o0[rest]) and torch.equal(lse[rest], l0[rest]), row
+
+
+# ------------------------------------------------------------------------------------ races between written pages
+def test_append_of_a_long_run_is_checked_in_its_time(tpc):
+    """A prompt of 100,000 tokens in 16-token pages, 6,250 written pages that are all compared: with a status word
+    the append takes at most three quarters longer than without."""
+    import torch
+    n, page = 100_000, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    table = torch.randperm(n // page, generator=g, device="cuda").int()[None]
+    cache = torch.zeros(n // page, page, 576, dtype=torch.bfloat16, device="cuda")
+    x = torch.randn(n, 576, generator=g, device="cuda").bfloat16()
+    kv, start, status = i32([n]), i32([0, n]), new_status()
+
+    def us(**kw):
+        times = []
+        for _ in range(8):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            tpc.tpc_latent_append(cache, table, kv, x[:, :512], x[:, 512:], row_start=start, **kw)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b) * 1e3)
+        return sorted(times)[2]
+
+    plain, checked = us(), us(status=status)
+    assert status.item() == 0
+    assert checked < 1.75 * plain, (plain, checked)
+    # the same page at both ends of the run, and next to each other
+    for a, b in ((0, n // page - 1), (3, 4), (17, 4000)):
+        t = table.clone()
+        t[0, a] = t[0, b]
+        status.zero_()
+        tpc.tpc_latent_append(cache, t, kv, x[:, :512], x[:, 512:], row_start=start, status=status)
+        assert status.item() == 7, (a, b)
+
+
+@pytest.mark.parametrize("m", [[1] * 70, [40] * 70, [1] * 31 + [900] + [1] * 38, [0] * 40 + [300, 0, 300] + [1] * 40, [17, 0, 1, 500]])
+def test_append_races_between_any_two_sequences(tpc, m):
+    """Sequences of few and of many pages: a page that any two of them write, or one twice, is found wherever it
+    stands; pages that are shared but not written are none."""
+    import torch
+    rng = np.random.default_rng(sum(m))
+    page, B, n = 16, len(m), sum(m)
+    kv = [x + int(rng.integers(0, 40)) if x else 33 for x in m]
+    per = max(-(-L // page) for L in kv)
+    x = torch.zeros(n, 576, dtype=torch.bfloat16, device="cuda")
+    cache = torch.zeros(B * per, page, 576, dtype=torch.bfloat16, device="cuda")
+    sound = rng.permutation(B * per).reshape(B, per).astype(np.int32)
+    written = [(b, p) for b in range(B) if m[b] for p in range((kv[b] - m[b]) // page, -(-kv[b] // page))]
+    kept = [(b, p) for b in range(B) for p in range(0, (kv[b] - m[b]) // page)]
+
+    def status_of(t):
+        status = new_status()
+        tpc.tpc_latent_append(cache, i32(t), i32(kv), x[:, :512], x[:, 512:], row_start=i32(starts(m)), status=status)
+        return status.item()
+
+    assert status_of(sound) == 0
+    shared = sound.copy()
+    for b, p in kept:
+        shared[b, p] = sound[kept[0]]
+    assert status_of(shared) == 0
+    pairs = [rng.choice(len(written), 2, replace=False) for _ in range(12)] + [(0, len(written) - 1), (len(written) - 2, len(written) - 1)]
+    for i, j in pairs:
+        t = sound.copy()
+        t[written[i]] = t[written[j]]
+        assert status_of(t) == 7, (written[i], written[j])

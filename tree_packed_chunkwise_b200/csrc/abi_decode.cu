@@ -123,12 +123,13 @@ int tpc_latent_append(const tpc_latent_cache* cache, const tpc_rows* rows, const
   const tpc::AppendArgs a{lc, r, c, kr, ld_c, ld_kr, status};
   constexpr int per = tpc::kAppendThreads / 32;
   const unsigned grid = (unsigned)(((int64_t)r.n_rows + per - 1) / per);
-  if (in_dtype == TPC_BF16) {
-    TPC_LAUNCH("latent_append", st, (tpc::latent_append_kernel<bf><<<grid, tpc::kAppendThreads, 0, st>>>(a)));
-  } else {
-    TPC_LAUNCH("latent_append", st, (tpc::latent_append_kernel<float><<<grid, tpc::kAppendThreads, 0, st>>>(a)));
-  }
-  return TPC_OK;
+  auto go = [&](auto tin, auto check) -> int {
+    TPC_LAUNCH("latent_append", st,
+               (tpc::latent_append_kernel<decltype(tin), decltype(check)::value><<<grid, tpc::kAppendThreads, 0, st>>>(a)));
+    return TPC_OK;
+  };
+  auto with_check = [&](auto tin) { return status ? go(tin, std::true_type{}) : go(tin, std::false_type{}); };
+  return in_dtype == TPC_BF16 ? with_check(bf{}) : with_check(float{});
 }
 
 int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld_q, const void* w_b, void* qa,
