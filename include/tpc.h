@@ -628,8 +628,9 @@ int tpc_latent_absorb(const tpc_rows* rows, int32_t H, const void* q, int64_t ld
  *   scratch: tpc_latent_attn_scratch_bytes(H) bytes, 256-byte aligned, used by one call at a time.
  * Deterministic: the same call gives the same bits (the pieces that a long context is summed in depend
  * on the whole batch, so another batch may round a sequence differently).  A block table entry outside 0 .. n_pages - 1
- * or a kv_len beyond max_pages * page_size records TPC_ERR_DEVICE_CHECK (the sequence's rows are
- * then unspecified).
+ * stands for a page of zeros, a kv_len beyond max_pages * page_size is cut to it; both record
+ * TPC_ERR_DEVICE_CHECK (without a status word nothing does: the sequence's rows are wrong, but hold nothing
+ * of other sequences).
  */
 size_t tpc_latent_attn_scratch_bytes(int32_t H);
 int tpc_latent_attn(const tpc_latent_cache* cache, const tpc_rows* rows, int32_t H, float scale, const void* qa,

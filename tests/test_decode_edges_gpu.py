@@ -467,3 +467,26 @@ def test_append_races_between_any_two_sequences(tpc, m):
         t = sound.copy()
         t[written[i]] = t[written[j]]
         assert status_of(t) == 7, (written[i], written[j])
+
+
+# ------------------------------------------------------------------------------------ pages outside the cache
+@pytest.mark.parametrize("entry", [-1, 48, 2 ** 31 - 1])
+@pytest.mark.parametrize("H", [16, 24, 40])
+def test_attention_of_pages_outside_the_cache_reads_no_other_page(tpc, entry, H):
+    """An entry outside the cache, with or without a status word: the outputs of its sequence are unspecified, but
+    they do not depend on what other sequences' pages hold."""
+    import torch
+    rng = np.random.default_rng(H)
+    cache, _ = rounded(rng, 48, 64, 576, dtype=torch.bfloat16)
+    qa, _ = rounded(rng, 1, H, 576, dtype=torch.bfloat16)
+    table = np.arange(20, 40, dtype=np.int32)[None]
+    table[0, [0, 7, 19]] = entry
+    rest = torch.ones(48, dtype=torch.bool, device="cuda")
+    rest[20:40] = False
+    rest[[20, 27, 39]] = True
+    got = []
+    for fill in (1.0, -2.0, float("nan")):
+        cache[rest] = fill
+        got.append(tpc.tpc_latent_attn(qa, cache, i32(table), i32([1250]), SCALE))
+    for o, lse in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])

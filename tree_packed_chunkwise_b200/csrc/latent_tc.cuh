@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
     while (cur.valid && ok) {
       if (cur.page < 0 || cur.page >= a.cache.n_pages) {
         set_status(a.status, kStatusCheck);
-        cur.page = 0;
+        cur.page = a.cache.n_pages;  // past the tensor map's end: the copies read zeros, no other sequence's tokens
+        cur.off = 0;
       }
       const int my_row = cur.page * ps + cur.off;
       if (cur.first) {
