@@ -76,7 +76,7 @@ __device__ __forceinline__ bool bad_row_starts(const DecodeRows& r, int64_t at, 
 }
 
 // 10000^(-2 i / 64) / (2 pi), the turns per position of the rotary pair i, as powers of 10000^(-1 / 32) (their
-// rounding errors stay below i 2^-53 of a value that shrinks by a quarter per i).  A table in memory:
+// relative errors, with the ratio's own, stay below (2 i + 1) 2^-53, of a value that shrinks by a quarter per i).  A table in memory:
 // lane i's load takes the time of the others beside it, a power in double precision more.
 struct RopeTurns {
   double t[kLatRope / 2];
@@ -145,12 +145,12 @@ constexpr int kStepThreads = 128;
 // The columns of S evolve independently: with Sd = Diag(e^g) S, u = Sd^T k and w = Sd^T q,
 //   delta = beta (v - u),  S' = Sd + k delta^T,  o = S'^T q = w + (k . q) delta,
 // so one pass over a column does everything: a state is read once and written once, and their bytes
-// bound the step (4 flops a byte).
+// bound the step (7 flops for the 8 bytes of an element).
 //
 // A lane holds R rows x 4 columns of one head's state in registers, a warp 4 CG columns; sums over the
 // rows are shuffles, and nothing is shared between warps (no barrier, so runs of rows and small batches
-// are as short as their loads).  CG neighbouring lanes read 16 CG consecutive bytes of a row: 64 (d = 128)
-// or 128.  Many bytes in flight matter most: at d = 128, 512 sequences of 32 heads, bf16 rows, 16 rows
+// are as short as their loads).  CG neighbouring lanes read 16 CG consecutive bytes of a row: 64 (d = 128
+// and 64) or 128.  Many bytes in flight matter most: at d = 128, 512 sequences of 32 heads, bf16 rows, 16 rows
 // a lane and 4 CTAs an SM take 324 us (6.69 TB/s, of a measured copy rate of 6.56), 3 CTAs 353 us, 8 rows
 // and 6 CTAs 370 us, 8 rows unbounded 439 us, and a ring of TMA copies through shared memory 352 us.
 // d = 64 at 2000 sequences 329 us (6.51 TB/s), d = 32 86 us (6.36 TB/s).
