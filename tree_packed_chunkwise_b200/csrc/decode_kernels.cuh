@@ -54,17 +54,21 @@ __device__ __forceinline__ bool rows_ok(const DecodeRows& r, int first, int end)
 // the sequence and position of row t, by the whole warp
 __device__ __forceinline__ RowAt row_at(const DecodeRows& r, int t) {
   if (!r.row_start) return {t, (int64_t)r.kv_len[t] - 1};
-  auto owns = [&](int b) { return t >= r.row_start[b] && t < r.row_start[b + 1] && rows_ok(r, r.row_start[b], r.row_start[b + 1]); };
+  auto owns = [&](int first, int end) { return t >= first && t < end && rows_ok(r, first, end); };
   int b = seq_of_row(r.row_start, r.n_seqs, t);
   if (b >= r.n_seqs) return {-1, 0};
-  if (!owns(b)) {  // no sequence's row, or the search was misled by a table that decreases somewhere
+  int first = r.row_start[b], end = r.row_start[b + 1], kv = r.kv_len[b];
+  if (!owns(first, end)) {  // no sequence's row, or the search was misled by a table that decreases somewhere
     uint32_t found = 0;
     const int lane = threadIdx.x & 31;
-    for (b = lane; !found && b - lane < r.n_seqs; b += 32) found = __ballot_sync(0xffffffffu, b < r.n_seqs && owns(b));
+    for (b = lane; !found && b - lane < r.n_seqs; b += 32)
+      found = __ballot_sync(0xffffffffu, b < r.n_seqs && owns(r.row_start[b], r.row_start[b + 1]));
     if (!found) return {-1, 0};
     b = b - lane - 32 + __ffs(found) - 1;
+    end = r.row_start[b + 1];
+    kv = r.kv_len[b];
   }
-  return {b, (int64_t)r.kv_len[b] - r.row_start[b + 1] + t};
+  return {b, (int64_t)kv - end + t};
 }
 
 // Whether a sequence of this thread's (every `of`-th from `at`) has rows outside 0 .. n_rows
