@@ -534,7 +534,7 @@ int tpc_group_status(const tpc_plan* plan, const tpc_group_shape* shape, void* w
  * negative position (kv_len 0: a padding entry of the batch) has no token.  A sequence whose rows are
  * not within 0 .. n_rows, or whose row_start decreases, is skipped and recorded.  row_start, kv_len and
  * the block table are device memory, read when the kernels run, so that a captured graph can be
- * replayed with new values.
+ * replayed with new values.  They are read several times in a call and must not change while it runs.
  *
  * status (optional device int) receives TPC_ERR_DEVICE_CHECK if an index is outside its range (the
  * entry is then skipped or bounded, never followed) and TPC_ERR_TIMEOUT if a bounded wait ran out.

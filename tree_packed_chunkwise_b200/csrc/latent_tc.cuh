@@ -277,7 +277,7 @@ __device__ __forceinline__ void round_to_smem(const uint32_t (&r)[32], uint8_t* 
 // the old maximum stay valid, which saves the pass over O^T.
 //
 // 64 contexts of 16,384 tokens, 16 heads: 213 us (5.67 TB/s of cache, 86 % of the copy rate; copies alone
-// 186 us), 32 heads (NT = 32, half the tokens) 130 us.  Runs of 300 rows over 4,096 tokens (NT = 64): 450
+// 186 us), 32 heads (NT = 32, half the tokens) 130 us.  Runs of 300 rows over 4,096 tokens (NT = 64): 440
 // TFLOP/s (without the low parts 490, the rows' bound being the chain of scores, softmax and weighted sum).
 // Kernel times of 64 contexts of 4,000 tokens with 16, 32 and 64 columns a tile: one row of 16 heads (16
 // columns used) 65, 73 and 92 us; 2 rows 105, 75 and 92; 4 rows 214, 126 and 94.
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kLatAttnThreads, 1)
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // latent_combine_kernel waits for this grid's end itself
   const uint32_t tb = *tslot;
-  LatWalk<NT> walk(a, *where, where->b < 0 ? 0 : share);  // (< 0: the lengths changed under the call)
+  LatWalk<NT> walk(a, *where, where->b < 0 ? 0 : share);  // (< 0: no start was found: lengths changed, which they must not)
   auto aborted = [&] { return *((volatile int*)abort_flag) != 0; };
   // Every wait is bounded.  After the first that runs out no role waits any more; the producer stops, the
   // others walk on to the end of their loops, so the barriers between the softmax warps match.
