@@ -60,8 +60,9 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // The kernels' waits are bounded by a limit of their arguments; with 0 they give up at once, so that the ways
-// out can be tested (the attention, whose waits cost time, starts as if one had run out).  What a CTA waits for on its way out (its copies to land, its MMAs to complete) is
-// bounded by kWayOutNs instead, whatever the limit.
+// out can be tested (the attention, whose waits cost time, starts as if one had run out).  What a CTA waits
+// for on its way out (its copies to land, its MMAs to complete) is bounded by kWayOutNs instead, whatever the
+// limit.
 constexpr uint64_t kWayOutNs = 2000000000ull;
 __device__ __forceinline__ bool mbar_wait_limit(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   return limit_ns ? mbar_wait(bar, parity, limit_ns) : mbar_test_wait(bar, parity);
@@ -269,10 +270,10 @@ __device__ __forceinline__ void round_to_smem(const uint32_t (&r)[32], uint8_t* 
 // leaves partial sums for latent_combine_kernel.
 //
 // Warp 0 fetches tiles by TMA (64-column boxes, one per page and column chunk) into the ring (a prefetch
-// of the next tile into L2 beside it measured 2 % slower).  Warp 1 issues the MMAs: the scores of tile i + 1 as far as its slots have arrived, and the weighted sum of
-// tile i as soon as the weights are there.  Warps 2-5 run the softmax: a warp holds KT / 4 tokens x NT
-// columns of S^T in the 16x256b register layout, maxima over tokens are 3 shuffles and one exchange
-// between the four warps.  Running sums stay per lane until the piece ends.  A column's maximum is only
+// of the next tile into L2 beside it measured 2 % slower).  Warp 1 issues the MMAs: the scores of tile i + 1
+// as far as its slots have arrived, and the weighted sum of tile i as soon as the weights are there.  Warps
+// 2-5 run the softmax: a warp holds KT / 4 tokens x NT columns of S^T in the 16x256b register layout, maxima
+// over tokens are 3 shuffles and one exchange between the four warps.  Running sums stay per lane until the piece ends.  A column's maximum is only
 // raised when it grew by more than 8 (base 2): until then its weights are at most 2^8 and the sums of
 // the old maximum stay valid, which saves the pass over O^T.
 //
